@@ -26,6 +26,8 @@ DEVERR_WAIT_TIMEOUT = 1
 DEVERR_PAGE_RANGE = 2
 DEVERR_SLOT_RANGE = 4
 DEVERR_PLAN_MISMATCH = 8
+DEVERR_POS_RANGE = 16
+DEVERR_SEQ_RANGE = 32
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libisoquant.so")
@@ -37,7 +39,8 @@ SYMBOLS = [
     "isoquant_attend_partial", "isoquant_attend_combine", "isoquant_get_status", "isoquant_last_launch_count",
     "isoquant_attend_decode_static", "isoquant_decode_prep", "isoquant_step_workspace_size",
     "isoquant_decode_step", "isoquant_init_bits", "isoquant_codebook_bits", "isoquant_selftest_wait",
-    "isoquant_workspace_size_paged", "isoquant_debug_export_z",
+    "isoquant_workspace_size_paged", "isoquant_debug_export_z", "isoquant_decode_prep_rope", "isoquant_dense_prep",
+    "isoquant_dense_workspace_size", "isoquant_dense_attend", "isoquant_prompt_attend",
 ]
 
 
@@ -52,6 +55,16 @@ class _Cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
+class _DenseCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 def lib():
     """Load libisoquant.so (raises if it is missing: no fallback path)."""
     global _lib
@@ -62,6 +75,9 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         cp = ctypes.POINTER(_Cache)
+        dp = ctypes.POINTER(_DenseCache)
+        rp = ctypes.POINTER(_Rope)
+        i64 = ctypes.c_int64
         sig = {
             "isoquant_init": ([ctypes.POINTER(vp), i32, i32, vp, vp], i32),
             "isoquant_init_bits": ([ctypes.POINTER(vp), i32, i32, vp, vp, i32], i32),
@@ -89,6 +105,13 @@ def lib():
                                       ctypes.c_float, vp, sz, vp, vp], i32),
             "isoquant_selftest_wait": ([vp, ctypes.c_uint64, vp, vp], i32),
             "isoquant_debug_export_z": ([vp, vp, i32, i32, vp, vp], i32),
+            "isoquant_decode_prep_rope": ([vp, cp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, rp, vp, vp], i32),
+            "isoquant_dense_prep": ([vp, dp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, rp, vp, vp, vp], i32),
+            "isoquant_dense_workspace_size": ([vp, i32, i32, i32, ctypes.POINTER(sz)], i32),
+            "isoquant_dense_attend": ([vp, dp, vp, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float, vp, sz, vp, vp],
+                                      i32),
+            "isoquant_prompt_attend": ([vp, vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, i32, i32, ctypes.c_float,
+                                        vp, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -170,6 +193,52 @@ class PagedCache:
         return _Cache(self.codes.data_ptr(), self.norms.data_ptr(), self.num_pages, self.page_size)
 
 
+class DenseCache:
+    """Caller-owned paged cache of 16-bit keys and values: bfloat16 or float16
+    [pages][2 (K,V)][H][page_size][128]."""
+
+    def __init__(self, data, page_size):
+        assert data.dtype in (torch.bfloat16, torch.float16) and data.is_contiguous()
+        assert data.dim() == 5 and data.shape[1] == 2 and data.shape[3] == page_size and data.shape[4] == HEAD_DIM
+        self.data = data
+        self.num_kv_heads = data.shape[2]
+        self.num_pages = data.shape[0]
+        self.page_size = page_size
+        self._c = _DenseCache(data.data_ptr(), _dtype(data), self.num_pages, page_size)
+
+    @staticmethod
+    def allocate(num_kv_heads, num_pages, page_size, dtype=torch.bfloat16, device="cuda"):
+        return DenseCache(torch.zeros((num_pages, 2, num_kv_heads, page_size, HEAD_DIM), dtype=dtype, device=device),
+                          page_size)
+
+    def c_struct(self):
+        return self._c
+
+
+class Rope:
+    """Rotation by position: a float32 table [positions][rot_dim] (the cosines
+    of a position's rot_dim / 2 angles, then the sines) and which coordinates
+    pair up: (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved."""
+
+    def __init__(self, cos_sin, rot_dim=HEAD_DIM, interleaved=False):
+        assert cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
+        assert cos_sin.dim() == 2 and cos_sin.shape[1] == rot_dim
+        self.cos_sin = cos_sin
+        self.rot_dim = rot_dim
+        self.interleaved = bool(interleaved)
+        self._c = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], rot_dim, int(self.interleaved))
+
+    @staticmethod
+    def table(num_positions, rot_dim=HEAD_DIM, base=10000.0, device="cuda"):
+        """The table of angles position * base^(-2i / rot_dim), taken in 64 bits."""
+        inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+        ang = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * inv
+        return torch.cat([ang.cos(), ang.sin()], 1).float()
+
+    def c_struct(self):
+        return self._c
+
+
 # ----------------------------------------------------------------- C ABI calls
 def isoquant_init(signs, quats, head_dim=HEAD_DIM, bits=3):
     """signs: int8 [H][128] (+-1); quats: float32 [H][32][2][4] (host arrays);
@@ -230,6 +299,101 @@ def isoquant_decode_prep(ctx, cache, k, v, slot_mapping, q, q_rot, stream=None):
     _check(lib().isoquant_decode_prep(ctx.handle, ctypes.byref(cs), _ptr(k), _ptr(v), k.shape[0], _ptr(slot_mapping),
                                       _ptr(q), _dtype(q), q.shape[0], q.shape[1], _ptr(q_rot), _stream(stream)),
            "isoquant_decode_prep")
+
+
+def _positions(t, n):
+    assert t.dtype == torch.int64 and t.is_contiguous() and t.numel() == n
+
+
+def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_rot, stream=None):
+    """isoquant_decode_prep with keys rotated to positions k_pos (int64
+    [n_tok]) before they are compressed and query rows to q_pos (int64
+    [n_rows]) before R; rope: Rope."""
+    assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
+    assert q.is_contiguous() and q_rot.is_contiguous() and q_rot.dtype == torch.float32 and q_rot.shape == q.shape
+    assert k.dtype == v.dtype == q.dtype
+    _positions(slot_mapping, k.shape[0])
+    _positions(k_pos, k.shape[0])
+    _positions(q_pos, q.shape[0])
+    cs = cache.c_struct()
+    _check(lib().isoquant_decode_prep_rope(ctx.handle, cs, _ptr(k), _ptr(v), k.shape[0], _ptr(slot_mapping),
+                                           _ptr(k_pos), _ptr(q), _dtype(q), q.shape[0], q.shape[1], _ptr(q_pos),
+                                           rope.c_struct(), _ptr(q_rot), _stream(stream)),
+           "isoquant_decode_prep_rope")
+
+
+def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_out, k_out=None, stream=None):
+    """Append keys rotated to k_pos and values ([n_tok][H][128], bf16 or fp16)
+    to a DenseCache and write the queries ([n_rows][Hq][128]) rotated to q_pos
+    into q_out, in one launch; k_out (same shape as k, may be k itself)
+    receives the rotated keys of every token.  rope None: no rotation (the
+    positions may be None).  cache None: only k_out and q_out are written (v
+    and slot_mapping may be None)."""
+    assert k.is_contiguous() and q.is_contiguous() and q_out.is_contiguous()
+    assert k.dtype == q.dtype == q_out.dtype and q_out.shape == q.shape
+    assert k.dim() == 3 and k.shape[1] == ctx.num_kv_heads and k.shape[2] == HEAD_DIM
+    assert q.dim() == 3 and q.shape[2] == HEAD_DIM
+    if cache is not None:
+        assert v.is_contiguous() and v.shape == k.shape and v.dtype == k.dtype
+        assert cache.num_kv_heads == ctx.num_kv_heads
+        _positions(slot_mapping, k.shape[0])
+    if rope is not None:
+        _positions(k_pos, k.shape[0])
+        _positions(q_pos, q.shape[0])
+    if k_out is not None:
+        assert k_out.is_contiguous() and k_out.shape == k.shape and k_out.dtype == k.dtype
+    _check(lib().isoquant_dense_prep(ctx.handle, cache.c_struct() if cache is not None else None, _ptr(k), _ptr(v),
+                                     k.shape[0], _ptr(slot_mapping), _ptr(k_pos), _ptr(q), _dtype(q), q.shape[0],
+                                     q.shape[1], _ptr(q_pos), rope.c_struct() if rope is not None else None,
+                                     _ptr(k_out), _ptr(q_out), _stream(stream)), "isoquant_dense_prep")
+
+
+def isoquant_dense_workspace_size(ctx, batch, nq, num_q_heads):
+    n = ctypes.c_size_t()
+    _check(lib().isoquant_dense_workspace_size(ctx.handle, batch, nq, num_q_heads, ctypes.byref(n)),
+           "isoquant_dense_workspace_size")
+    return n.value
+
+
+def alloc_dense_workspace(ctx, batch, nq, num_q_heads, device="cuda"):
+    n = isoquant_dense_workspace_size(ctx, batch, nq, num_q_heads)
+    return torch.empty(((n + 15) // 16) * 4, dtype=torch.int32, device=device)
+
+
+def isoquant_dense_attend(ctx, cache, q, page_table, seq_lens, workspace, out, causal=False, scale=0.0, stream=None):
+    """Attention of the newest tokens over a DenseCache: q and out
+    [B][nq][Hq][128] of the cache's dtype; page_table int32 [B][max_pages];
+    seq_lens int32 [B]; workspace from alloc_dense_workspace."""
+    assert q.is_contiguous() and q.dim() == 4 and q.shape[3] == HEAD_DIM and q.dtype == cache.data.dtype
+    assert out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
+    assert page_table.dtype == torch.int32 and page_table.is_contiguous() and page_table.shape[0] == q.shape[0]
+    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() == q.shape[0]
+    assert cache.num_kv_heads == ctx.num_kv_heads
+    B, nq, Hq, _ = q.shape
+    _check(lib().isoquant_dense_attend(ctx.handle, cache.c_struct(), _ptr(q), B, nq, Hq, _ptr(page_table),
+                                       page_table.shape[1], _ptr(seq_lens), int(bool(causal)), float(scale),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
+                                       _stream(stream)), "isoquant_dense_attend")
+
+
+def isoquant_prompt_attend(ctx, q, k, v, cu_seqlens, out, causal=True, scale=0.0, stream=None):
+    """Attention of packed prompts to themselves: q, out [T][Hq][128] and k, v
+    [T][H][128] (bf16 or fp16; q, k and v may be slices of one projection:
+    tokens any multiple of 8 elements apart, heads contiguous); cu_seqlens
+    int32 [batch + 1]."""
+    for t in (q, k, v):
+        assert t.dim() == 3 and t.shape[2] == HEAD_DIM and t.stride(2) == 1
+        assert t.shape[1] == 1 or t.stride(1) == HEAD_DIM
+    assert k.shape[1] == v.shape[1] == ctx.num_kv_heads and q.shape[0] == k.shape[0] == v.shape[0]
+    assert q.dtype == k.dtype == v.dtype == out.dtype
+    assert out.is_contiguous() and out.shape == q.shape
+    assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 1
+    T, Hq, _ = q.shape
+    # a single token's stride is arbitrary
+    qs, ks, vs = ((t.stride(0) if T > 1 else t.shape[1] * HEAD_DIM) for t in (q, k, v))
+    _check(lib().isoquant_prompt_attend(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _dtype(q), T, Hq, qs, ks, vs,
+                                        _ptr(cu_seqlens), cu_seqlens.numel() - 1, int(bool(causal)), float(scale),
+                                        _ptr(out), _stream(stream)), "isoquant_prompt_attend")
 
 
 def isoquant_step_workspace_size(ctx, batch, nq, num_q_heads):

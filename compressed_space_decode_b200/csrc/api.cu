@@ -175,6 +175,20 @@ int dtype_bytes(int dtype) {
   }
 }
 
+int check_rope(const isoquant_rope *rope) {
+  if (rope == nullptr || rope->cos_sin == nullptr || rope->num_positions < 1) return ISOQUANT_ERR_INVALID_ARG;
+  if (rope->rot_dim < 32 || rope->rot_dim > kD || rope->rot_dim % 32 != 0) return ISOQUANT_ERR_UNSUPPORTED;
+  return aligned(rope->cos_sin, 16) ? ISOQUANT_OK : ISOQUANT_ERR_ALIGNMENT;
+}
+
+bool is_16bit(int dtype) { return dtype == ISOQUANT_BF16 || dtype == ISOQUANT_F16; }
+
+int check_dense_cache(const isoquant_dense_cache *cache) {
+  if (cache == nullptr || cache->data == nullptr || cache->num_pages < 1) return ISOQUANT_ERR_INVALID_ARG;
+  if (!is_16bit(cache->dtype) || !valid_page_size(cache->page_size)) return ISOQUANT_ERR_UNSUPPORTED;
+  return aligned(cache->data, 16) ? ISOQUANT_OK : ISOQUANT_ERR_ALIGNMENT;
+}
+
 }  // namespace
 }  // namespace isoquant
 
@@ -349,6 +363,156 @@ int isoquant_decode_prep(isoquant_ctx *ctx, const isoquant_cache *cache, const v
   if (st != ISOQUANT_OK) return st;
   cudaError_t e = launch_decode_prep(ctx, cache, k, v, n_tok, slot_mapping, q, dtype, n_rows, num_q_heads, q_rot,
                                      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return ISOQUANT_ERR_CUDA;
+  ctx->last_launches = 1;
+  return ISOQUANT_OK;
+}
+
+int isoquant_decode_prep_rope(isoquant_ctx *ctx, const isoquant_cache *cache, const void *k, const void *v, int n_tok,
+                              const int64_t *slot_mapping, const int64_t *k_pos, const void *q, int dtype, int n_rows,
+                              int num_q_heads, const int64_t *q_pos, const isoquant_rope *rope, float *q_rot,
+                              void *stream) {
+  ISOQUANT_TRACE("isoquant_decode_prep_rope");
+  if (ctx == nullptr || n_tok < 0 || n_rows < 0 || num_q_heads < 1) return ISOQUANT_ERR_INVALID_ARG;
+  ctx->last_launches = 0;
+  int st = check_cache(cache);
+  if (st != ISOQUANT_OK) return st;
+  st = check_rope(rope);
+  if (st != ISOQUANT_OK) return st;
+  if (num_q_heads % ctx->num_kv_heads != 0) return ISOQUANT_ERR_INVALID_ARG;
+  const int eb = dtype_bytes(dtype);
+  if (eb == 0) return ISOQUANT_ERR_UNSUPPORTED;
+  const uintptr_t need = eb == 4 ? 16 : 8;
+  if (n_tok > 0) {
+    if (k == nullptr || v == nullptr || slot_mapping == nullptr || k_pos == nullptr) return ISOQUANT_ERR_INVALID_ARG;
+    if (!aligned(k, need) || !aligned(v, need) || !aligned(slot_mapping, 8) || !aligned(k_pos, 8))
+      return ISOQUANT_ERR_ALIGNMENT;
+  }
+  if (n_rows > 0) {
+    if (q == nullptr || q_rot == nullptr || q_pos == nullptr) return ISOQUANT_ERR_INVALID_ARG;
+    // query vectors and their warps are counted in 32 bits
+    if (static_cast<int64_t>(n_rows) * num_q_heads >= INT32_MAX) return ISOQUANT_ERR_INVALID_ARG;
+    if (!aligned(q, need) || !aligned(q_rot, 16) || !aligned(q_pos, 8)) return ISOQUANT_ERR_ALIGNMENT;
+  }
+  if (n_tok == 0 && n_rows == 0) return ISOQUANT_OK;
+  st = check_device(ctx);
+  if (st != ISOQUANT_OK) return st;
+  cudaError_t e = launch_decode_prep_rope(ctx, cache, k, v, n_tok, slot_mapping, k_pos, q, dtype, n_rows, num_q_heads,
+                                          q_pos, rope, q_rot, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return ISOQUANT_ERR_CUDA;
+  ctx->last_launches = 1;
+  return ISOQUANT_OK;
+}
+
+int isoquant_dense_prep(isoquant_ctx *ctx, const isoquant_dense_cache *cache, const void *k, const void *v, int n_tok,
+                        const int64_t *slot_mapping, const int64_t *k_pos, const void *q, int dtype, int n_rows,
+                        int num_q_heads, const int64_t *q_pos, const isoquant_rope *rope, void *k_out, void *q_out,
+                        void *stream) {
+  ISOQUANT_TRACE("isoquant_dense_prep");
+  if (ctx == nullptr || n_tok < 0 || n_rows < 0 || num_q_heads < 1) return ISOQUANT_ERR_INVALID_ARG;
+  ctx->last_launches = 0;
+  int st = ISOQUANT_OK;
+  if (cache != nullptr) st = check_dense_cache(cache);
+  if (st != ISOQUANT_OK) return st;
+  if (rope != nullptr) st = check_rope(rope);
+  if (st != ISOQUANT_OK) return st;
+  if (num_q_heads % ctx->num_kv_heads != 0) return ISOQUANT_ERR_INVALID_ARG;
+  if (!is_16bit(dtype) || (cache != nullptr && cache->dtype != dtype)) return ISOQUANT_ERR_UNSUPPORTED;
+  if (n_tok > 0) {
+    if (k == nullptr || (cache == nullptr && k_out == nullptr)) return ISOQUANT_ERR_INVALID_ARG;
+    if (cache != nullptr && (v == nullptr || slot_mapping == nullptr)) return ISOQUANT_ERR_INVALID_ARG;
+    if (rope != nullptr && k_pos == nullptr) return ISOQUANT_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(k_out, 16)) return ISOQUANT_ERR_ALIGNMENT;
+    if (cache != nullptr && (!aligned(v, 16) || !aligned(slot_mapping, 8))) return ISOQUANT_ERR_ALIGNMENT;
+    if (rope != nullptr && !aligned(k_pos, 8)) return ISOQUANT_ERR_ALIGNMENT;
+  }
+  if (n_rows > 0) {
+    if (q == nullptr || q_out == nullptr || (rope != nullptr && q_pos == nullptr)) return ISOQUANT_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || (rope != nullptr && !aligned(q_pos, 8)))
+      return ISOQUANT_ERR_ALIGNMENT;
+  }
+  // (token, head) pairs are counted in 32 bits
+  if (static_cast<int64_t>(n_rows) * num_q_heads + 2 * static_cast<int64_t>(n_tok) * ctx->num_kv_heads >= INT32_MAX)
+    return ISOQUANT_ERR_INVALID_ARG;
+  if (n_tok == 0 && n_rows == 0) return ISOQUANT_OK;
+  st = check_device(ctx);
+  if (st != ISOQUANT_OK) return st;
+  cudaError_t e = launch_dense_prep(ctx, cache, k, v, n_tok, slot_mapping, k_pos, q, dtype, n_rows, num_q_heads, q_pos,
+                                    rope, k_out, q_out, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return ISOQUANT_ERR_CUDA;
+  ctx->last_launches = 1;
+  return ISOQUANT_OK;
+}
+
+int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq, int num_q_heads, size_t *bytes) {
+  if (ctx == nullptr || bytes == nullptr) return ISOQUANT_ERR_INVALID_ARG;
+  AttendShape s;
+  int st = make_shape(ctx, batch, nq, num_q_heads, 256, 0, &s);
+  if (st != ISOQUANT_OK) return st;
+  *bytes = dense_workspace_bytes(s);
+  return ISOQUANT_OK;
+}
+
+int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache, const void *q, int batch, int nq,
+                          int num_q_heads, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
+                          int causal, float scale, void *workspace, size_t ws_bytes, void *out, void *stream) {
+  ISOQUANT_TRACE("isoquant_dense_attend");
+  if (ctx == nullptr) return ISOQUANT_ERR_INVALID_ARG;
+  ctx->last_launches = 0;
+  int st = check_dense_cache(cache);
+  if (st != ISOQUANT_OK) return st;
+  AttendShape s;
+  st = make_shape(ctx, batch, nq, num_q_heads, cache->page_size, causal, &s);
+  if (st != ISOQUANT_OK) return st;
+  if (!(scale >= 0.0f) || !std::isfinite(scale)) return ISOQUANT_ERR_INVALID_ARG;
+  if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(kD));
+  if (batch == 0) return ISOQUANT_OK;
+  if (q == nullptr || page_table == nullptr || seq_lens == nullptr || workspace == nullptr || out == nullptr ||
+      max_pages < 1)
+    return ISOQUANT_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4))
+    return ISOQUANT_ERR_ALIGNMENT;
+  if (ws_bytes < dense_workspace_bytes(s)) return ISOQUANT_ERR_WORKSPACE;
+  st = check_device(ctx);
+  if (st != ISOQUANT_OK) return st;
+  cudaError_t e = launch_dense_attend(ctx, cache, s, q, page_table, max_pages, seq_lens, scale, workspace, out,
+                                      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return ISOQUANT_ERR_CUDA;
+  ctx->last_launches = 2;
+  return ISOQUANT_OK;
+}
+
+int isoquant_prompt_attend(isoquant_ctx *ctx, const void *q, const void *k, const void *v, int dtype, int n_tok,
+                           int num_q_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const int32_t *cu_seqlens, int batch, int causal, float scale, void *out, void *stream) {
+  ISOQUANT_TRACE("isoquant_prompt_attend");
+  if (ctx == nullptr || n_tok < 0 || batch < 0 || num_q_heads < 1) return ISOQUANT_ERR_INVALID_ARG;
+  ctx->last_launches = 0;
+  const int H = ctx->num_kv_heads;
+  if (num_q_heads % H != 0) return ISOQUANT_ERR_INVALID_ARG;
+  if (!is_16bit(dtype) || num_q_heads / H > 128) return ISOQUANT_ERR_UNSUPPORTED;
+  if (!(scale >= 0.0f) || !std::isfinite(scale)) return ISOQUANT_ERR_INVALID_ARG;
+  if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(kD));
+  if (n_tok == 0 || batch == 0) return ISOQUANT_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || cu_seqlens == nullptr || out == nullptr)
+    return ISOQUANT_ERR_INVALID_ARG;
+  // strides reach the copies as bytes, below 2^40; (token, head) pairs and
+  // work items are counted in 32 bits
+  const int64_t kMaxStride = int64_t(1) << 38;
+  if (q_stride < static_cast<int64_t>(num_q_heads) * kD || k_stride < static_cast<int64_t>(H) * kD ||
+      v_stride < static_cast<int64_t>(H) * kD || q_stride > kMaxStride || k_stride > kMaxStride ||
+      v_stride > kMaxStride)
+    return ISOQUANT_ERR_INVALID_ARG;
+  if ((static_cast<int64_t>(n_tok) + batch) * num_q_heads >= INT32_MAX) return ISOQUANT_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 4) ||
+      q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return ISOQUANT_ERR_ALIGNMENT;
+  const int st = check_device(ctx);
+  if (st != ISOQUANT_OK) return st;
+  cudaError_t e = launch_prompt_attend(ctx, q, k, v, dtype, n_tok, num_q_heads, q_stride, k_stride, v_stride,
+                                       cu_seqlens, batch, causal ? 1 : 0, scale, out,
+                                       static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return ISOQUANT_ERR_CUDA;
   ctx->last_launches = 1;
   return ISOQUANT_OK;

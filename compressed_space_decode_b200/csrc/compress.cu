@@ -59,8 +59,8 @@ __device__ __forceinline__ void rotate_f32(const HeadParams &hp, int lane, const
   }
 }
 
-__device__ __forceinline__ void rotate_f64(const HeadParams &hp, int lane, const float (&x)[4],
-                                           double (&out)[4]) {
+template <typename X>
+__device__ __forceinline__ void rotate_f64(const HeadParams &hp, int lane, const X (&x)[4], double (&out)[4]) {
   const uint32_t sn = lane_sign_nibble(hp, lane);
   double y[4];
 #pragma unroll
@@ -70,6 +70,52 @@ __device__ __forceinline__ void rotate_f64(const HeadParams &hp, int lane, const
 #pragma unroll
   for (int r = 0; r < 4; ++r)
     out[r] = fma(m[4 * r + 3], y[3], fma(m[4 * r + 2], y[2], fma(m[4 * r + 1], y[1], m[4 * r] * y[0])));
+}
+
+// ------------------------------------------------------ position rotation
+// Position p turns the pair (a, b) of coordinates (i, i + rot / 2), or
+// (2i, 2i + 1) if `inter`, into (a c - b s, b c + a s), with c = table[p][i]
+// and s = table[p][rot / 2 + i] (fp32); coordinates from rot on stay.  rot is
+// a multiple of 32, so that both coordinates of a pair lie in one layout-A
+// lane of the compress path (16m + 2q, 16m + 2q + 1) and whole lanes of the
+// four-coordinate layout rotate or stay.
+struct RopeArgs {
+  const float *table;  // [num_pos][rot]
+  const int64_t *k_pos, *q_pos;
+  int64_t num_pos;
+  int rot, inter;
+};
+
+// Four coordinates 4 lane .. 4 lane + 3 of a warp's vector, in the
+// arithmetic of X (float, or double with exact products of fp32 values).
+template <typename X>
+__device__ __forceinline__ void rope4(const RopeArgs &r, int64_t pos, int lane, const float (&x)[4], X (&y)[4]) {
+  const float *row = r.table + pos * r.rot;
+  const int half = r.rot >> 1, j = 4 * lane;
+  if (r.inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = x[i];
+    if (j < r.rot) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const X c = row[(j + i) >> 1], s = row[half + ((j + i) >> 1)];
+        y[i] = fma(X(x[i]), c, -(X(x[i + 1]) * s));
+        y[i + 1] = fma(X(x[i + 1]), c, X(x[i]) * s);
+      }
+    }
+    return;
+  }
+  // the partner coordinates are half / 4 lanes up (first half) or down
+  const bool rotates = j < r.rot, lower = j < half;
+  const int partner = !rotates ? lane : lower ? lane + (half >> 2) : lane - (half >> 2);
+  const int base = !rotates ? 0 : lower ? j : j - half;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const X o = __shfl_sync(0xffffffffu, x[i], partner);
+    const X c = row[base + i], s = row[half + base + i];
+    const X t = lower ? -(o * s) : o * s;
+    y[i] = rotates ? fma(X(x[i]), c, t) : X(x[i]);
+  }
 }
 
 struct CompressArgs {
@@ -150,6 +196,49 @@ __device__ __forceinline__ void unpack_a(const RawA<float> &r, const uint32_t (&
     a[m] = make_float2(__uint_as_float(__float_as_uint(r.w[m].x) ^ (sgn[m] << 16)),
                        __uint_as_float(__float_as_uint(r.w[m].y) ^ (sgn[m] & 0x80000000u)));
 }
+// The signs D on unpacked coordinates (the position rotation comes before
+// them, so a rotated key cannot take them at unpacking).
+__device__ __forceinline__ void sign_a(const uint32_t (&sgn)[8], float2 (&a)[8]) {
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    a[m].x = __uint_as_float(__float_as_uint(a[m].x) ^ (sgn[m] << 16));
+    a[m].y = __uint_as_float(__float_as_uint(a[m].y) ^ (sgn[m] & 0x80000000u));
+  }
+}
+// The position rotation of a layout-A lane's coordinates by table row `row`:
+// HM = rot / 32 rows m of the pair's first coordinates.  fp32: a c - fl(b s)
+// in one fma, so the rotated vector is off by at most 2 * 2^-24 of its norm.
+template <int HM>
+__device__ __forceinline__ void rope_a_rot(const float *row, int q, int inter, float2 (&a)[8]) {
+  if (inter) {
+#pragma unroll
+    for (int m = 0; m < 2 * HM; ++m) {
+      const float c = row[8 * m + q], s = row[16 * HM + 8 * m + q];
+      const float2 t = a[m];
+      a[m].x = fmaf(t.x, c, -(t.y * s));
+      a[m].y = fmaf(t.y, c, t.x * s);
+    }
+    return;
+  }
+#pragma unroll
+  for (int m = 0; m < HM; ++m) {
+    const float2 c = *reinterpret_cast<const float2 *>(row + 16 * m + 2 * q);
+    const float2 s = *reinterpret_cast<const float2 *>(row + 16 * HM + 16 * m + 2 * q);
+    const float2 lo = a[m], hi = a[m + HM];
+    a[m] = __ffma2_rn(lo, c, __fmul2_rn(hi, make_float2(-s.x, -s.y)));
+    a[m + HM] = __ffma2_rn(hi, c, __fmul2_rn(lo, s));
+  }
+}
+__device__ __forceinline__ void rope_a(const RopeArgs &r, int64_t pos, int q, float2 (&a)[8]) {
+  const float *row = r.table + pos * r.rot;
+  switch (r.rot) {
+    case 32: rope_a_rot<1>(row, q, r.inter, a); break;
+    case 64: rope_a_rot<2>(row, q, r.inter, a); break;
+    case 96: rope_a_rot<3>(row, q, r.inter, a); break;
+    default: rope_a_rot<4>(row, q, r.inter, a); break;
+  }
+}
+
 // sum of the lane's 16 squares (signs do not matter): pairs, then a tree
 __device__ __forceinline__ float lane_squares(const float2 (&a)[8]) {
   float2 s[4];
@@ -288,11 +377,11 @@ __device__ __forceinline__ void pack_store_wide(uint64_t cbits, int q, bool stor
 // The fp64 path for one vector, by the whole warp (lane l: coordinates
 // 4l..4l+3): norm, rotation and codes all in fp64.  Used for the few vectors
 // whose fp16 norm rounding or codes the fp32 fast path cannot decide.
-template <typename T, int BITS>
-__device__ void compress_one_fp64(const HeadParams &hp, const Codebook &cb, const T *src, uint32_t *codes,
+// X is the type its inputs are held in: float as loaded, double once rotated
+// by position (the products are exact there, their difference is not).
+template <int BITS, typename X>
+__device__ void compress_one_fp64(const HeadParams &hp, const Codebook &cb, const X (&xv)[4], uint32_t *codes,
                                   uint16_t *norms, int64_t block, int off, int ps_shift, int lane) {
-  float xv[4];
-  load4(src + 4 * lane, xv);
   double ss = static_cast<double>(xv[0]) * xv[0] + static_cast<double>(xv[1]) * xv[1] +
               static_cast<double>(xv[2]) * xv[2] + static_cast<double>(xv[3]) * xv[3];
 #pragma unroll
@@ -344,8 +433,11 @@ __device__ void compress_one_fp64(const HeadParams &hp, const Codebook &cb, cons
 // Warp w of the K (kv = 0) or V (kv = 1) half: rotate, quantize and pack
 // tokens strip * (w / H) .. + strip - 1 of head w % H, four at a time.
 // `tile` is the warp's shared tile (kTileFloats floats).
-template <typename T, int BITS>
-__device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uint32_t w, int lane, float *tile) {
+// ROPE: keys are rotated by position first (r), and a token whose position is
+// outside the table is skipped like one with a bad slot.
+template <typename T, int BITS, bool ROPE = false>
+__device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uint32_t w, int lane, float *tile,
+                                              const RopeArgs &r = RopeArgs{}) {
   constexpr int kHalf = 1 << (BITS - 1);  // codes below kHalf are the negative levels
   constexpr int kPos = kHalf - 1;         // positive thresholds (the middle one is 0)
   constexpr uint32_t kAll = (1u << BITS) - 1u;
@@ -373,25 +465,43 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
   // the inputs and slot of the group's next vector are loaded one iteration
   // ahead, so that their latency overlaps the current vector's rotation
   RawA<T> nraw{};
-  int64_t nslot = -1;
+  int64_t nslot = -1, npos = 0;
   if (t_begin + grp < t_end) {
     nslot = g.slots[t_begin + grp];
+    if constexpr (ROPE) npos = r.k_pos[t_begin + grp];
     load_a(src + (static_cast<int64_t>(t_begin + grp) * H + h) * kD, q, nraw);
   }
   for (int tb = t_begin; tb < t_end; tb += 4) {
     const int t = tb + grp;
     const bool live = t < t_end;
     float2 a[8];
-    int64_t slot = -1;
+    int64_t slot = -1, pos = 0;
     if (live) {
       slot = nslot;
-      unpack_a(nraw, lc.sgn, a);
+      if constexpr (ROPE) {
+        pos = npos;
+        if (slot >= 0 && (pos < 0 || pos >= r.num_pos)) {
+          if (q == 0) set_status(g.status, ISOQUANT_DEVERR_POS_RANGE);
+          slot = -1;
+        }
+        if (kv == 0) {
+          const uint32_t none[8] = {};
+          unpack_a(nraw, none, a);
+          if (slot >= 0) rope_a(r, pos, q, a);
+          sign_a(lc.sgn, a);
+        } else {
+          unpack_a(nraw, lc.sgn, a);
+        }
+      } else {
+        unpack_a(nraw, lc.sgn, a);
+      }
     } else {
 #pragma unroll
       for (int m = 0; m < 8; ++m) a[m] = make_float2(0.f, 0.f);
     }
     if (t + 4 < t_end) {
       nslot = g.slots[t + 4];
+      if constexpr (ROPE) npos = r.k_pos[t + 4];
       load_a(src + (static_cast<int64_t>(t + 4) * H + h) * kD, q, nraw);
     }
     const int64_t page = slot >> ps_shift;
@@ -402,8 +512,8 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
     // (4 levels in the lane, 3 across the group) is within 7 * 2^-24
     // relative; n32 = sqrt of it by sqrt.approx (within 2^-22), so n32 is
     // within ~5e-7 of the exact norm.  Its fp16 rounding is decided from
-    // n32's bits: fp16 keeps the top 10 of fp32's 23 mantissa bits, so the
-    // 13 below them place n32 inside an fp16 step, whose rounding midpoint
+    // n32's bits (a rotation by position adds 2 * 2^-24 = 1.2e-7): fp16 keeps
+    // the top 10 of fp32's 23 mantissa bits, so the 13 below them place n32 inside an fp16 step, whose rounding midpoint
     // is 0x1000.  A pattern 16 or more fp32 units from it lies at least
     // 2^-20 (9.5e-7) relative from the midpoint, so the exact norm rounds
     // the same way; closer, or outside the fp16 normal range below 65000
@@ -509,9 +619,17 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
       const int tv = tb + gv;
       const int64_t sl = __shfl_sync(0xffffffffu, slot, src_lane);
       const int64_t pg = sl >> ps_shift;
-      compress_one_fp64<T, BITS>(hp, cb, src + (static_cast<int64_t>(tv) * H + h) * kD, g.codes, g.norms,
-                                 (pg * 2 + kv) * H + h, static_cast<int>(sl & ((1 << ps_shift) - 1)), ps_shift,
-                                 lane);
+      const int so = static_cast<int>(sl & ((1 << ps_shift) - 1));
+      float xv[4];
+      load4(src + (static_cast<int64_t>(tv) * H + h) * kD + 4 * lane, xv);
+      if constexpr (ROPE) {
+        const int64_t pv = __shfl_sync(0xffffffffu, pos, src_lane);
+        double yv[4] = {xv[0], xv[1], xv[2], xv[3]};
+        if (kv == 0) rope4(r, pv, lane, xv, yv);
+        compress_one_fp64<BITS>(hp, cb, yv, g.codes, g.norms, (pg * 2 + kv) * H + h, so, ps_shift, lane);
+      } else {
+        compress_one_fp64<BITS>(hp, cb, xv, g.codes, g.norms, (pg * 2 + kv) * H + h, so, ps_shift, lane);
+      }
     }
   }
 }
@@ -588,8 +706,11 @@ struct RotateArgs {
 };
 
 // q_rot = R q for query vector `vec` (row vec / Hq, head vec % Hq).
-template <typename T>
-__device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, int lane) {
+// ROPE: q is rotated by position first; a row whose position is outside the
+// table is written as zeros.
+template <typename T, bool ROPE = false>
+__device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, int lane,
+                                            const RopeArgs &r = RopeArgs{}, uint32_t *status = nullptr) {
   const HeadParams *__restrict__ params = g.params;
   const T *__restrict__ q = static_cast<const T *>(g.q);
   const int n_rows = g.n_rows, Hq = g.Hq, G = g.G;
@@ -598,6 +719,19 @@ __device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, i
   const int hq = static_cast<int>(vec % static_cast<uint32_t>(Hq));
   float x[4], y[4];
   load4(q + static_cast<int64_t>(vec) * kD + 4 * lane, x);
+  if constexpr (ROPE) {
+    const int64_t pos = r.q_pos[vec / static_cast<uint32_t>(Hq)];
+    if (pos < 0 || pos >= r.num_pos) {
+      if (lane == 0) set_status(status, ISOQUANT_DEVERR_POS_RANGE);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = 0.f;
+    } else {
+      float xr[4];
+      rope4(r, pos, lane, x, xr);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = xr[i];
+    }
+  }
   rotate_f32(params[hq / G], lane, x, y);
   const float s = 0.08838834764831845f;  // 1/sqrt(128): the normalisation of Hn
   *reinterpret_cast<float4 *>(out + static_cast<int64_t>(vec) * kD + 4 * lane) = make_float4(y[0] * s, y[1] * s, y[2] * s, y[3] * s);
@@ -626,6 +760,25 @@ __global__ void __launch_bounds__(256) k_decode_prep(const CompressArgs c, const
     compress_warp<T, BITS>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * (blockDim.x >> 5) + warp, lane, tile[warp]);
   } else {
     rotate_warp<T>(r, static_cast<uint32_t>(bx - 2 * nbc) * (blockDim.x >> 5) + warp, lane);
+  }
+}
+
+// k_decode_prep with the position rotation in both halves.
+template <typename T, int BITS>
+__global__ void __launch_bounds__(256) k_decode_prep_rope(const CompressArgs c, const RotateArgs r,
+                                                          const RopeArgs rope, int nbc) {
+  __shared__ __align__(16) float tile[8][kTileFloats];
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int bx = static_cast<int>(blockIdx.x);
+  if (bx < 2 * nbc) {
+    const int kv = bx >= nbc ? 1 : 0;
+    compress_warp<T, BITS, true>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * (blockDim.x >> 5) + warp, lane,
+                                 tile[warp], rope);
+  } else {
+    rotate_warp<T, true>(r, static_cast<uint32_t>(bx - 2 * nbc) * (blockDim.x >> 5) + warp, lane, rope, c.status);
   }
 }
 
@@ -713,6 +866,16 @@ cudaError_t launch_prep_t(int dtype, dim3 grid, dim3 block, cudaStream_t stream,
     default: return launch_pdl(k_decode_prep<__half, BITS>, grid, block, 0, stream, c, r, nb);
   }
 }
+template <int BITS>
+cudaError_t launch_prep_rope_t(int dtype, dim3 grid, dim3 block, cudaStream_t stream, const CompressArgs &c,
+                               const RotateArgs &r, const RopeArgs &rope, int nb) {
+  switch (dtype) {
+    case ISOQUANT_F32: return launch_pdl(k_decode_prep_rope<float, BITS>, grid, block, 0, stream, c, r, rope, nb);
+    case ISOQUANT_BF16:
+      return launch_pdl(k_decode_prep_rope<__nv_bfloat16, BITS>, grid, block, 0, stream, c, r, rope, nb);
+    default: return launch_pdl(k_decode_prep_rope<__half, BITS>, grid, block, 0, stream, c, r, rope, nb);
+  }
+}
 }  // namespace
 
 cudaError_t launch_compress(const isoquant_ctx *ctx, const isoquant_cache *cache, const void *k,
@@ -780,6 +943,27 @@ cudaError_t launch_decode_prep(const isoquant_ctx *ctx, const isoquant_cache *ca
     case 2: return launch_prep_t<2>(dtype, grid, block, stream, c, r, nb);
     case 4: return launch_prep_t<4>(dtype, grid, block, stream, c, r, nb);
     default: return launch_prep_t<3>(dtype, grid, block, stream, c, r, nb);
+  }
+}
+
+cudaError_t launch_decode_prep_rope(const isoquant_ctx *ctx, const isoquant_cache *cache, const void *k,
+                                    const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
+                                    const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
+                                    const isoquant_rope *rope, float *q_rot, cudaStream_t stream) {
+  const int64_t nbc = compress_blocks(ctx, n_tok, 8);
+  const int64_t nbr = rotate_blocks(n_rows, num_q_heads);
+  const int64_t blocks = 2 * nbc + nbr;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const CompressArgs c = compress_args(ctx, cache, k, v, n_tok, slot_mapping);
+  const RotateArgs r = rotate_args(ctx, q, n_rows, num_q_heads, q_rot);
+  const RopeArgs ra{rope->cos_sin, k_pos, q_pos, rope->num_positions, rope->rot_dim, rope->interleaved};
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  const int nb = static_cast<int>(nbc);
+  switch (ctx->codebook.bits) {
+    case 2: return launch_prep_rope_t<2>(dtype, grid, block, stream, c, r, ra, nb);
+    case 4: return launch_prep_rope_t<4>(dtype, grid, block, stream, c, r, ra, nb);
+    default: return launch_prep_rope_t<3>(dtype, grid, block, stream, c, r, ra, nb);
   }
 }
 

@@ -73,6 +73,20 @@ cudaError_t launch_decode_prep(const isoquant_ctx *ctx, const isoquant_cache *ca
                                const void *v, int n_tok, const int64_t *slot_mapping, const void *q,
                                int dtype, int n_rows, int num_q_heads, float *q_rot, cudaStream_t stream);
 
+cudaError_t launch_decode_prep_rope(const isoquant_ctx *ctx, const isoquant_cache *cache, const void *k,
+                                    const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
+                                    const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
+                                    const isoquant_rope *rope, float *q_rot, cudaStream_t stream);
+// 16-bit cache and prompt attention (dense.cu, prompt.cu)
+cudaError_t launch_dense_prep(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const void *k,
+                              const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
+                              const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
+                              const isoquant_rope *rope, void *k_out, void *q_out, cudaStream_t stream);
+cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const void *k, const void *v, int dtype,
+                                 int n_tok, int num_q_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 const int32_t *cu_seqlens, int batch, int causal, float scale, void *out,
+                                 cudaStream_t stream);
+
 struct AttendShape {
   int batch, nq, q_heads, kv_heads, group, rows, row_groups, page_size, causal;
   int bits;  // code width of the context
@@ -96,6 +110,10 @@ cudaError_t launch_attend_partial(const isoquant_ctx *ctx, const isoquant_cache 
 cudaError_t launch_attend_combine(const isoquant_ctx *ctx, const AttendShape &s,
                                   const int32_t *seq_lens, const void *ws, size_t ws_bytes, float *out,
                                   cudaStream_t stream);
+size_t dense_workspace_bytes(const AttendShape &s);
+cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const AttendShape &s,
+                                const void *q, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
+                                float scale, void *ws, void *out, cudaStream_t stream);
 cudaError_t launch_wait_selftest(const isoquant_ctx *ctx, uint64_t limit_ns, uint64_t *elapsed_ns,
                                  cudaStream_t stream);
 

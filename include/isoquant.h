@@ -64,6 +64,8 @@ typedef enum {
 #define ISOQUANT_DEVERR_SLOT_RANGE 4u     /* slot_mapping entry outside the cache */
 #define ISOQUANT_DEVERR_PLAN_MISMATCH 8u  /* attend_combine given another workspace size than
                                              attend_partial: records not merged, zeros written */
+#define ISOQUANT_DEVERR_POS_RANGE 16u     /* position outside the rotation table */
+#define ISOQUANT_DEVERR_SEQ_RANGE 32u     /* cu_seqlens entry decreasing or outside the tokens */
 
 typedef enum {
   ISOQUANT_F32 = 0,
@@ -87,6 +89,36 @@ typedef struct {
   int32_t num_pages;
   int32_t page_size;
 } isoquant_cache;
+
+/* Rotation by position (rotary embedding), applied to keys and queries before
+ * anything else: position p turns the pair (a, b) of coordinates (i, i +
+ * rot_dim/2) -- or (2i, 2i+1) if `interleaved` is nonzero -- into
+ * (a c - b s, b c + a s), c = cos_sin[p][i], s = cos_sin[p][rot_dim/2 + i],
+ * i < rot_dim/2; coordinates from rot_dim on are left alone.
+ *   cos_sin: device float [num_positions][rot_dim], 16-byte aligned,
+ *            caller-owned: the cosines of a position's angles, then the
+ *            sines (angles of far positions want 64-bit arithmetic before
+ *            they are rounded into the table).
+ * rot_dim must be 32, 64, 96 or 128. */
+typedef struct {
+  const float *cos_sin;
+  int32_t num_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} isoquant_rope;
+
+/* Paged cache of uncompressed 16-bit keys and values, caller-owned device
+ * memory, for layers that stay uncompressed and as the yardstick of the
+ * packed cache:
+ *   data: `dtype` (BF16 or F16) [num_pages][2 (K,V)][num_kv_heads][page_size][128]
+ * Pages, slots and page tables as in isoquant_cache; 16-byte aligned.  The
+ * context gives the head count; its rotation and code width do not matter. */
+typedef struct {
+  void *data;
+  int32_t dtype;
+  int32_t num_pages;
+  int32_t page_size;
+} isoquant_dense_cache;
 
 /* Create a context for `num_kv_heads` heads on the current CUDA device.
  *   head_dim: must be 128 (RotaryQuant, Abstract: 256 parameters per head
@@ -227,6 +259,102 @@ int isoquant_decode_prep(isoquant_ctx *ctx, const isoquant_cache *cache,
                          const int64_t *slot_mapping, const void *q, int dtype,
                          int n_rows, int num_q_heads, float *q_rot,
                          void *stream);
+
+/* isoquant_decode_prep with the rotation by position on the way: keys become
+ * rope(k, k_pos) before they are compressed and queries rope(q, q_pos)
+ * before R; values are not rotated.
+ *   k_pos: device int64 [n_tok], q_pos: device int64 [n_rows] (query row r
+ *          holds all heads of one token), 8-byte aligned.
+ * Codes and norms are those of the rotated key in exact arithmetic on the
+ * fp32 table (it is not rounded to `dtype` in between).  A position outside
+ * the table sets ISOQUANT_DEVERR_POS_RANGE: that token is not appended, that
+ * q_rot row is zeros.  Positions of tokens with a negative slot are not
+ * looked at.  Errors: as isoquant_decode_prep; INVALID_ARG (null rope, table
+ * or positions, num_positions < 1), UNSUPPORTED (rot_dim), ALIGNMENT. */
+int isoquant_decode_prep_rope(isoquant_ctx *ctx, const isoquant_cache *cache,
+                              const void *k, const void *v, int n_tok,
+                              const int64_t *slot_mapping,
+                              const int64_t *k_pos, const void *q, int dtype,
+                              int n_rows, int num_q_heads,
+                              const int64_t *q_pos, const isoquant_rope *rope,
+                              float *q_rot, void *stream);
+
+/* The same preparation for a 16-bit cache, in one launch: append
+ * rope(k, k_pos) and v at their slots and write q_out = rope(q, q_pos), each
+ * computed in fp32 and rounded once to `dtype` (BF16 or F16, the cache's).
+ *   k, v, slot_mapping, q: as isoquant_decode_prep, 16-byte aligned
+ *   rope:  NULL appends and copies without a rotation; k_pos and q_pos are
+ *          then not looked at and may be NULL
+ *   k_out: device [n_tok][num_kv_heads][128] of `dtype` or NULL: every
+ *          token's rotated key, negative slots included (the keys
+ *          isoquant_prompt_attend and isoquant_compress_kv want)
+ *   q_out: device, shaped as q
+ *   cache: may be NULL, then only k_out and q_out are written (v and
+ *          slot_mapping are not looked at)
+ * k_out may be k and q_out may be q; otherwise buffers must not overlap.
+ * Either half may be empty.  A position outside the table sets
+ * ISOQUANT_DEVERR_POS_RANGE: that token is not appended and its k_out or
+ * q_out row is zeros.  Errors: INVALID_ARG, UNSUPPORTED (dtype, page size,
+ * rot_dim), ALIGNMENT, CUDA. */
+int isoquant_dense_prep(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
+                        const void *k, const void *v, int n_tok,
+                        const int64_t *slot_mapping, const int64_t *k_pos,
+                        const void *q, int dtype, int n_rows, int num_q_heads,
+                        const int64_t *q_pos, const isoquant_rope *rope,
+                        void *k_out, void *q_out, void *stream);
+
+/* Workspace bytes isoquant_dense_attend needs. */
+int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq,
+                                  int num_q_heads, size_t *bytes);
+
+/* Attention of each sequence's newest tokens over a 16-bit paged cache,
+ * split over the context and joined: o = sum_t p_t v_t, p = softmax of
+ * scale <q, k_t> over the visible tokens; scores, softmax statistics and
+ * sums in fp32, the result rounded once.
+ *   q:   device [batch][nq][num_q_heads][128] of the cache's dtype,
+ *        16-byte aligned (rotated by position already, if at all)
+ *   out: device, same shape and dtype, 16-byte aligned
+ *   page_table, max_pages, seq_lens, causal, scale: as
+ *        isoquant_attend_decode, tokens behind seq_lens[b] are not looked at
+ *   workspace: device, >= isoquant_dense_workspace_size bytes, 16-byte
+ *        aligned; its contents on entry do not matter; calls whose kernels
+ *        overlap on the GPU must not share one workspace
+ * A row that sees no token outputs zeros.  Two kernel launches.  Errors:
+ * INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
+int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
+                          const void *q, int batch, int nq, int num_q_heads,
+                          const int32_t *page_table, int max_pages,
+                          const int32_t *seq_lens, int causal, float scale,
+                          void *workspace, size_t ws_bytes, void *out,
+                          void *stream);
+
+/* Attention of whole prompts to themselves, several prompts of any lengths
+ * packed one after another, on keys and values as they come from the
+ * projections (before they are compressed or appended).
+ *   q: device [n_tok][num_q_heads][128] of `dtype` (BF16 or F16), k, v:
+ *      device [n_tok][num_kv_heads][128]; heads contiguous, tokens q_stride,
+ *      k_stride and v_stride elements apart (multiples of 8, at least the
+ *      heads' extent), 16-byte aligned
+ *   cu_seqlens: device int32 [batch + 1]: sequence b is tokens
+ *      cu_seqlens[b] .. cu_seqlens[b + 1] - 1; empty ones are allowed.
+ *      Entries that decrease or leave [0, n_tok] set
+ *      ISOQUANT_DEVERR_SEQ_RANGE and that sequence is skipped
+ *   causal: if nonzero, a token sees itself and the tokens before it in its
+ *      sequence, otherwise its whole sequence
+ *   scale: softmax scale; 0 selects 1/sqrt(128)
+ *   out: device [n_tok][num_q_heads][128] of `dtype`, contiguous, 16-byte
+ *      aligned, apart from the inputs; rows of no sequence are left as they
+ *      were
+ * Scores, softmax statistics and sums in fp32; softmax weights are rounded
+ * to `dtype` for the product with v.  One kernel launch, no workspace.
+ * num_q_heads / num_kv_heads at most 128.  Errors: INVALID_ARG, UNSUPPORTED
+ * (dtype, group size), ALIGNMENT, CUDA. */
+int isoquant_prompt_attend(isoquant_ctx *ctx, const void *q, const void *k,
+                           const void *v, int dtype, int n_tok,
+                           int num_q_heads, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const int32_t *cu_seqlens,
+                           int batch, int causal, float scale, void *out,
+                           void *stream);
 
 /* Workspace bytes isoquant_decode_step needs: the attention workspace
  * rounded up to 256 bytes, then the rotated queries
