@@ -189,6 +189,11 @@ int check_dense_cache(const isoquant_dense_cache *cache) {
   return aligned(cache->data, 16) ? ISOQUANT_OK : ISOQUANT_ERR_ALIGNMENT;
 }
 
+// the attention counts a cache's rows of 128 in 32 bits
+bool dense_rows_fit(const isoquant_ctx *ctx, const isoquant_dense_cache *cache) {
+  return static_cast<int64_t>(cache->num_pages) * 2 * ctx->num_kv_heads * cache->page_size <= INT32_MAX;
+}
+
 }  // namespace
 }  // namespace isoquant
 
@@ -449,7 +454,7 @@ int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq, in
   AttendShape s;
   int st = make_shape(ctx, batch, nq, num_q_heads, 256, 0, &s);
   if (st != ISOQUANT_OK) return st;
-  *bytes = dense_workspace_bytes(s);
+  *bytes = dense_workspace_bytes(ctx, s);
   return ISOQUANT_OK;
 }
 
@@ -464,6 +469,7 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache, 
   AttendShape s;
   st = make_shape(ctx, batch, nq, num_q_heads, cache->page_size, causal, &s);
   if (st != ISOQUANT_OK) return st;
+  if (!dense_rows_fit(ctx, cache)) return ISOQUANT_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || !std::isfinite(scale)) return ISOQUANT_ERR_INVALID_ARG;
   if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(kD));
   if (batch == 0) return ISOQUANT_OK;
@@ -473,7 +479,7 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache, 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(page_table, 4) ||
       !aligned(seq_lens, 4))
     return ISOQUANT_ERR_ALIGNMENT;
-  if (ws_bytes < dense_workspace_bytes(s)) return ISOQUANT_ERR_WORKSPACE;
+  if (ws_bytes < dense_workspace_bytes(ctx, s)) return ISOQUANT_ERR_WORKSPACE;
   st = check_device(ctx);
   if (st != ISOQUANT_OK) return st;
   cudaError_t e = launch_dense_attend(ctx, cache, s, q, page_table, max_pages, seq_lens, scale, workspace, out,

@@ -1,0 +1,1138 @@
+// attend16.cu -- attention on 16-bit queries, keys and values, head dim 128:
+// isoquant_prompt_attend (packed prompts to themselves) and
+// isoquant_dense_attend (newest tokens over the paged 16-bit cache, split over
+// the context and joined).
+//
+// One tcgen05 kernel serves both.  A row tile is up to 128 query rows of one
+// KV head: `tok` consecutive tokens times the group's heads, so that the heads
+// that share keys share each key tile.  Keys and values come as tiles of 128
+// tokens.  For a tile: S = Q K^T (8 products of 16 dims), an online softmax of
+// S's rows, O += P V (8 products of 16 tokens).
+//   * S[128 x 128] fp32 sits in tensor memory, lane = row.  A softmax thread
+//     owns a row: it takes its 128 scores into registers, and writes the
+//     weights P (16-bit pairs) over S's columns, from where they are the A
+//     operand of P V: neither S nor P passes through shared memory.
+//   * Two S/P/O sets ("sides"), each with a warpgroup of softmax threads, so
+//     that the tensor cores work for one side while the other's softmax runs.
+//     Prompts: the sides are two neighbouring row tiles that share the key
+//     tiles.  Cache: the sides take alternate key tiles of the same rows
+//     and are merged at the end of the sequence's part.
+//   * The products of a side are issued in order S(i), PV(i), S(i + 1), so a
+//     completed S(i + 1) also says that PV(i) is done, and a softmax thread may
+//     rescale its O row then.  It does so only when the row's maximum passed
+//     the reference by 2^8 (weights stay below 2^8, or 2^15 in fp16's scaled
+//     form, and the sums are fp32, so a late reference loses nothing).
+//   * A loader warp brings Q, K and V by TMA with the 128-byte swizzle that the
+//     products read; a ring of 32 KB slots takes key and value tiles in the
+//     order of their use.  Pages shorter than a tile are one box each.
+//   * Two guard warps clear, in value tiles that no row or not every row sees
+//     whole, the rows behind the last visible token (neighbouring sequences,
+//     padding, stale pages: 0 x NaN would be NaN) and non-finite
+//     elements; the rows that do see such an element get it added at the end.
+// All waits are bounded; after one expires every role leaves its loop.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <type_traits>
+
+#include "isoquant_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace isoquant {
+namespace {
+
+constexpr int kTile = 128;                  // rows of a row tile, tokens of a key tile
+constexpr int kTileBytes = kTile * kD * 2;  // 32 KB
+constexpr int kThreads16 = 3 * 128;         // two sides, then the MMA, loader and two guard warps
+constexpr int kMaxSlots = 6;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10;
+// shared memory: the tiles, then
+constexpr int kOffBad = 0;                        // first token with +inf, -inf, NaN of each dim
+constexpr int kOffMl = kOffBad + 3 * kD * 4;      // side 1's (reference, sum) of each row; first the locate scratch
+constexpr int kOffBar = kOffMl + kTile * 8;       // barriers
+constexpr int kNumBars = 2 * kMaxSlots + 2 + 2 + 2 + 2 + 2 + 6;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tensor-memory base, abort flag, MMA-issued flag, non-finite flag
+constexpr int kTailBytes = kOffMisc + 16;
+
+struct Attend16 {
+  int H, Hq, G, GB, chunks, tok, R, B, nq, causal;  // GB: heads of a row tile (G, or 128 of a larger group)
+  float c;                                          // softmax scale * log2(e)
+  const int32_t *cu;                                // prompts
+  int n_tok;
+  const int32_t *page_table, *seq_lens;             // cache
+  int max_pages, num_pages, ps_shift;
+  float *records;
+  int2 *plan;
+  int n_cta, row_stride;                            // records: rows rounded up to 2
+  int slots, q_half;                                // ring slots, bytes of a 64-dim half of a Q buffer
+  void *out;
+  uint32_t *status;
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// maximum of three that keeps a NaN
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __half) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// shared-memory matrix descriptor, 128-byte swizzle, strides in 16-byte units
+__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo) << 16) |
+         (static_cast<uint64_t>(sbo) << 32) | (1ull << 46) | (2ull << 61);
+}
+// A, B of type T (bf16 or fp16, both the same), fp32 accumulator, 128 x 128
+template <typename T>
+__device__ constexpr uint32_t idesc16(int b_mn_major) {
+  constexpr uint32_t t = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(b_mn_major) << 16) | ((128u >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u)
+      : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The reference passed by 2^kLazy moves; fp16 weights are held times 2^7 so
+// that those far below the maximum keep their bits (2^15 at most).
+constexpr float kLazy = 8.f;
+template <typename T>
+constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
+
+// One key tile of a softmax thread's row: scores at tensor-memory columns ts,
+// of which the first `vis` count, become weights 2^(c s - sub) at the same
+// columns; with kLo the weights' remainders follow as a second operand.
+template <typename T, bool kLo>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int vis, bool first, float &ref,
+                                             float &l) {
+  float s[4][32];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tmem_ld32_async(ts + 32 * k, s[k]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tmem_arrived(s[k]);
+  if (__any_sync(0xffffffffu, vis < kTile)) {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i)
+      if (i >= vis) s[i >> 5][i & 31] = -INFINITY;
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < kTile; i += 8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], s[i >> 5][(i + e) & 31], s[i >> 5][(i + e + 4) & 31]);
+  }
+  const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * c;
+  const bool move = !(mt <= ref + kLazy);  // a NaN moves too
+  if (__any_sync(0xffffffffu, move)) {
+    const float to_ref = move ? mt : ref;
+    const float corr = move ? ex2f(ref - to_ref) : 1.f;
+    ref = to_ref;
+    l *= corr;
+    if (!first) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float o[32];
+        tmem_ld32(to + 32 * k, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= corr;
+        tmem_st32(to + 32 * k, o);
+      }
+    }
+  }
+  const float sub = ref == -INFINITY ? 0.f : ref - kShift<T>;
+  const float2 c2 = make_float2(c, c), n2 = make_float2(-sub, -sub);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t w[16], r[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = __ffma2_rn(make_float2(s[k][i], s[k][i + 1]), c2, n2);
+      const float2 p = make_float2(ex2f(x.x), ex2f(x.y));
+      sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
+      w[i >> 1] = pack16(p.x, p.y, T());
+      if constexpr (kLo)
+        r[i >> 1] = pack16(p.x - __uint_as_float(w[i >> 1] << 16), p.y - __uint_as_float(w[i >> 1] & 0xffff0000u), T());
+    }
+    tmem_st16u(ts + 16 * k, w);
+    if constexpr (kLo) tmem_st16u(ts + 64 + 16 * k, r);
+  }
+  l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  tmem_stored();
+}
+
+// ---------------------------------------------------------------- the work
+// A segment: one sequence's (row tile, KV head) and a run of its key tiles.
+struct Segment {
+  int b, h;
+  int row0;         // first token of the row tile (of side 0) in its sequence's queries
+  int chunk;        // heads chunk * 128 .. of a group above 128
+  int kv0;          // prompts: first token of the sequence
+  int rows;         // prompts: tokens of the sequence; cache: nq
+  int shift;        // row of query token i sees tokens below i + shift (causal)
+  int cap;          // no row sees more
+  int j0, n[2];     // first key tile, tiles of each side (cache: n[0] = all, split even and odd)
+  int id;           // cache: segment number
+  bool whole;       // cache: all of the sequence's tiles
+  bool starts;      // cache: from tile 0
+  // tokens that query token i sees
+  __device__ int limit(int i, int causal) const { return causal ? max(0, min(cap, i + shift)) : cap; }
+};
+
+// cache: tiles of a row tile (one at least: its rows have to be written)
+struct Unit {
+  int b, rt, L, cap, row0, chunk, nt;
+  __device__ void set(const Attend16 &p, int u) {
+    const int rts = (p.nq + p.tok - 1) / p.tok * p.chunks;
+    b = u / rts;
+    rt = u - b * rts;
+    L = p.seq_lens[b];
+    const int64_t room = static_cast<int64_t>(p.max_pages) << p.ps_shift;
+    cap = max(0, static_cast<int>(min(static_cast<int64_t>(L), room)));
+    row0 = rt / p.chunks * p.tok;
+    chunk = rt % p.chunks;
+    const int last = min(p.nq, row0 + p.tok) - 1;
+    const int64_t hz = p.causal ? min(static_cast<int64_t>(cap), static_cast<int64_t>(L) - p.nq + last + 1) : cap;
+    nt = max(1, static_cast<int>((hz + kTile - 1) / kTile));
+  }
+};
+
+// The CTA's part [gs, ge) of all tiles, and the (unit, tile offset) where it
+// starts.  loc: {gs, ge, unit, offset, total}; ends with __syncthreads.
+__device__ void locate16(const Attend16 &p, int64_t *loc, int64_t *scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int U = p.B * ((p.nq + p.tok - 1) / p.tok * p.chunks);
+  const int u0 = static_cast<int>(static_cast<int64_t>(U) * tid / kThreads16),
+            u1 = static_cast<int>(static_cast<int64_t>(U) * (tid + 1) / kThreads16);
+  int64_t mine = 0;
+  Unit un;
+  for (int u = u0; u < u1; ++u) {
+    un.set(p, u);
+    mine += static_cast<int64_t>(un.nt) * p.H;
+    if (blockIdx.x == 0 && un.cap < un.L) set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads16 / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const int64_t excl = before + incl - mine;
+  const int64_t N = min(static_cast<int64_t>(p.n_cta), total), c = blockIdx.x;
+  const int64_t gs = c < N ? total * c / N : 0, ge = c < N ? total * (c + 1) / N : 0;
+  if (tid == 0) {
+    loc[0] = gs;
+    loc[1] = ge;
+    loc[4] = total;
+  }
+  if (gs < ge && excl <= gs && gs < excl + mine) {
+    int64_t run = excl;
+    for (int u = u0; u < u1; ++u) {
+      un.set(p, u);
+      const int64_t n = static_cast<int64_t>(un.nt) * p.H;
+      if (gs < run + n) {
+        loc[2] = u;
+        loc[3] = gs - run;
+        break;
+      }
+      run += n;
+    }
+  }
+  __syncthreads();
+}
+
+// cache: the segments of a CTA's part, in the same order for every role
+struct Walk16 {
+  int64_t g, ge;
+  Unit un;
+  int u, h, j;
+  __device__ Walk16(const Attend16 &p, const int64_t *loc) {
+    g = loc[0];
+    ge = loc[1];
+    if (g < ge) {
+      u = static_cast<int>(loc[2]);
+      un.set(p, u);
+      h = static_cast<int>(loc[3] / un.nt);
+      j = static_cast<int>(loc[3] - static_cast<int64_t>(h) * un.nt);
+    }
+  }
+  __device__ bool next(const Attend16 &p, Segment &s) {
+    if (g >= ge) return false;
+    if (j == un.nt) {
+      j = 0;
+      if (++h == p.H) {
+        h = 0;
+        un.set(p, ++u);
+      }
+    }
+    s.b = un.b;
+    s.h = h;
+    s.row0 = un.row0;
+    s.chunk = un.chunk;
+    s.kv0 = 0;
+    s.rows = p.nq;
+    s.shift = un.L - p.nq + 1;
+    s.cap = un.cap;
+    s.j0 = j;
+    s.n[0] = static_cast<int>(min(static_cast<int64_t>(un.nt - j), ge - g));
+    s.n[1] = 0;
+    s.id = u * p.H + h;
+    s.starts = j == 0;
+    j += s.n[0];
+    g += s.n[0];
+    s.whole = s.starts && j == un.nt;
+    return true;
+  }
+};
+
+// prompts: sequence and pair of row tiles of this CTA, found by one warp.
+// Pairs are counted from each sequence's last (the most keys) to its first,
+// the KV heads of a pair next to one another.  false: no work.
+__device__ bool find_prompt(const Attend16 &p, Segment &s) {
+  const int lane = threadIdx.x & 31;
+  const int item = static_cast<int>(blockIdx.x / p.H);
+  s.h = static_cast<int>(blockIdx.x % p.H);
+  int before = 0, highest = 0;
+  bool found = false;
+  for (int b0 = 0; b0 < p.B && (!found || blockIdx.x == 0); b0 += 32) {  // block 0 looks at all bounds
+    const int b = b0 + lane;
+    const int x = b < p.B ? p.cu[b] : 0, y = b < p.B ? p.cu[b + 1] : 0;
+    // the sequences lie one behind another: none starts before an earlier bound
+    int top = b < p.B ? x : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, top, o);
+      if (lane >= o) top = max(top, t);
+    }
+    const int earlier = max(highest, top);
+    const bool good = x >= 0 && y >= x && y <= p.n_tok && x >= earlier;
+    if (b < p.B && !good && blockIdx.x == 0) set_status(p.status, ISOQUANT_DEVERR_SEQ_RANGE);
+    const int pairs = b < p.B && good ? (y - x + 2 * p.tok - 1) / (2 * p.tok) : 0;
+    int incl = pairs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int first = before + incl - pairs;
+    const unsigned hit = __ballot_sync(0xffffffffu, item >= first && item < first + pairs);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s.b = b0 + src;
+      s.kv0 = __shfl_sync(0xffffffffu, x, src);
+      s.rows = __shfl_sync(0xffffffffu, y - x, src);
+      const int pair = __shfl_sync(0xffffffffu, first + pairs - 1 - item, src);
+      s.row0 = pair * 2 * p.tok;
+      found = true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    highest = max(highest, __shfl_sync(0xffffffffu, max(top, y), 31));
+  }
+  if (!found) return false;
+  s.chunk = 0;
+  s.shift = 1;
+  s.cap = s.rows;
+  s.j0 = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int lo = s.row0 + x * p.tok, hi = min(s.rows, lo + p.tok);
+    s.n[x] = lo < s.rows ? ((p.causal ? hi : s.rows) + kTile - 1) / kTile : 0;
+  }
+  return true;
+}
+
+// Every wait of a warp: false once it, or any other of the CTA, gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Attend16 &p, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, abort));
+}
+
+// 16-bit patterns whose exponent is all ones
+template <typename T>
+__device__ __forceinline__ uint32_t exponent_mask() {
+  return std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
+}
+
+// kPaged: the cache's form, else prompts.  kLo: bf16 weights as two operands
+// (16 bits), so that the result is off by one rounding.
+template <typename T, bool kPaged>
+__global__ void __launch_bounds__(kThreads16, 1)
+    k_attend16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv) {
+  constexpr bool kLo = kPaged && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t *ring = smem + 4 * p.q_half, *tail = ring + p.slots * kTileBytes;
+  int *bad = reinterpret_cast<int *>(tail + kOffBad);
+  float2 *ml = reinterpret_cast<float2 *>(tail + kOffMl);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(tail + kOffBar);
+  uint64_t *full = bars, *freed = bars + kMaxSlots, *q_full = bars + 2 * kMaxSlots, *q_free = q_full + 2,
+           *s_full = q_full + 4, *p_full = q_full + 6, *o_done = q_full + 8, *guarded = q_full + 10,
+           *side1 = guarded + 1, *seg_done = guarded + 2, *mma_done = guarded + 3, *cleared = guarded + 4, *guard_go = guarded + 5;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + kOffMisc);
+  volatile int *abort = reinterpret_cast<volatile int *>(tail + kOffMisc + 4);
+  volatile int *issued = reinterpret_cast<volatile int *>(tail + kOffMisc + 8);
+  volatile int *nonfinite = reinterpret_cast<volatile int *>(tail + kOffMisc + 12);
+  int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffMl);
+  const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+    tc_fence_before();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&freed[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], row_warps);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(guarded, 2);
+    mbar_init(side1, row_warps);
+    mbar_init(seg_done, row_warps);
+    mbar_init(mma_done, 1);
+    mbar_init(cleared, 1);
+    mbar_init(guard_go, 1);
+    *abort = 0;
+    *issued = 0;
+    *nonfinite = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = tid; i < 3 * kD; i += kThreads16) bad[i] = INT_MAX;
+  pdl_trigger();
+  pdl_wait();
+  Segment sg{};
+  if constexpr (kPaged) {
+    locate16(p, loc, loc + 8);
+  } else {
+    // every warp finds the CTA's work by itself
+    __syncthreads();
+  }
+  const bool has_prompt = kPaged ? false : find_prompt(p, sg);
+  int64_t my_loc[5];
+  if constexpr (kPaged) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) my_loc[i] = loc[i];
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // f(segment, number) for each segment of this CTA, until f says stop
+  auto for_segments = [&](auto &&f) {
+    if constexpr (kPaged) {
+      Walk16 wk(p, my_loc);
+      Segment s;
+      for (uint32_t k = 0; wk.next(p, s); ++k)
+        if (!f(s, k)) return;
+    } else {
+      if (has_prompt) f(sg, 0u);
+    }
+  };
+  // a segment's key tiles hold tokens 128 j ..; below this token every row sees all
+  auto all_see = [&](const Segment &s) { return s.limit(s.row0, p.causal); };
+  auto none_sees = [&](const Segment &s) {
+    const int last = min(s.rows, s.row0 + (kPaged ? 1 : 2) * p.tok) - 1;
+    return s.limit(last, p.causal);
+  };
+
+  // registers of the four helper warps go to the softmax threads:
+  // 256 x 208 + 128 x 80 of the 384 x 168 at launch
+  if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ------------------------------------------------------------------ MMA
+    const bool leader = lane == 0;
+    uint32_t slot = 0, round = 0;  // next ring slot in the order of use
+    uint32_t n_p[2] = {0, 0}, n_guard = 0;
+    bool ok = true;
+    auto take = [&]() {  // waits for the next slot's tile
+      ok = ok && warp_wait(&full[slot], round & 1u, p, abort);
+      const uint32_t s = slot;
+      if (++slot == static_cast<uint32_t>(p.slots)) {
+        slot = 0;
+        ++round;
+      }
+      return s;
+    };
+    const uint64_t dK = desc128(smem_addr(ring), 1, 64), dV = desc128(smem_addr(ring), kTileBytes / 32, 64);
+    const uint32_t q_units = static_cast<uint32_t>(p.q_half) >> 4;
+    auto issue_s = [&](int x, int qb, uint32_t sl) {
+      tc_fence_after();
+      if (leader && ok) {
+        *issued = 1;
+        const uint64_t a = desc128(smem_addr(smem), 1, 64) + static_cast<uint64_t>(qb) * 2 * q_units;
+        const uint64_t b = dK + sl * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + 128 * x, a + (k >> 2) * static_cast<uint64_t>(q_units) + 2 * (k & 3),
+                 b + (k >> 2) * (kTileBytes >> 5) + 2 * (k & 3), idesc16<T>(0), k > 0);
+        umma_commit(&s_full[x]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int x, uint32_t sl, bool first, bool guard) {
+      if (guard && ok && leader) mbar_arrive(guard_go);
+      __syncwarp();
+      ok = ok && warp_wait(&p_full[x], n_p[x] & 1u, p, abort);
+      ++n_p[x];
+      if (guard) {
+        ok = ok && warp_wait(guarded, n_guard & 1u, p, abort);
+        ++n_guard;
+      }
+      tc_fence_after();
+      if (leader && ok) {
+        const uint64_t b = dV + sl * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, b + 128 * k, idesc16<T>(1), !first || k > 0);
+        if constexpr (kLo) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * k, b + 128 * k, idesc16<T>(1), 1);
+        }
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t *bar) {
+      if (leader && ok) umma_commit(bar);
+      __syncwarp();
+    };
+    for_segments([&](const Segment &s, uint32_t k) {
+      const int all = all_see(s);
+      if constexpr (kPaged) {
+        const int n = s.n[0], qb = k & 1;
+        ok = ok && warp_wait(&q_full[qb], (k >> 1) & 1u, p, abort);
+        for (int i = 0; i < n + 2 && ok; ++i) {
+          const int x = i & 1;
+          if (i >= 2 && i - 2 < n) {
+            const int t0 = (s.j0 + i - 2) * kTile;
+            const uint32_t sl = take();
+            issue_pv(x, sl, i - 2 < 2, t0 + kTile > all);
+            commit(&freed[sl]);
+            if (i >= n) commit(&o_done[x]);
+          }
+          if (i < n) {
+            const uint32_t sl = take();
+            issue_s(x, qb, sl);
+            commit(&freed[sl]);
+            if (i == n - 1) commit(&q_free[qb]);
+          }
+        }
+      } else {
+        const int n = max(s.n[0], s.n[1]);
+        uint32_t v_slot = 0, k_slot = 0;
+        for (int j = 0; j <= n && ok; ++j) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int other = s.n[1 - x];
+            if (j > 0 && j - 1 < s.n[x]) {
+              // the first side to need a tile waits for it, the last frees it
+              if (x == 0 || j - 1 >= other) v_slot = take();
+              const bool first_user = x == 0 || j - 1 >= other;
+              issue_pv(x, v_slot, j == 1, first_user && j * kTile > all);
+              if (x == 1 || j - 1 >= other) commit(&freed[v_slot]);
+              if (j == s.n[x]) commit(&o_done[x]);
+            }
+            if (j < s.n[x]) {
+              if (j == 0) ok = ok && warp_wait(&q_full[x], 0, p, abort);
+              if (x == 0 || j >= other) k_slot = take();
+              issue_s(x, x, k_slot);
+              if (x == 1 || j >= other) commit(&freed[k_slot]);
+            }
+          }
+        }
+      }
+      return ok;
+    });
+    if (*issued) umma_commit_by(leader, mma_done);
+  } else if (warp == kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // --------------------------------------------------------------- loader
+    uint32_t slot = 0, round = 0;
+    bool ok = true;
+    auto next_slot = [&]() {  // waits until the next slot's last tile was used
+      if (round > 0) ok = ok && warp_wait(&freed[slot], (round + 1) & 1u, p, abort);
+      const uint32_t s = slot;
+      if (++slot == static_cast<uint32_t>(p.slots)) {
+        slot = 0;
+        ++round;
+      }
+      return s;
+    };
+    const uint32_t sq = smem_addr(smem), sr = smem_addr(ring);
+    // box of a Q tile: 64 dims x GB heads x tok tokens
+    auto load_q = [&](int qb, const Segment &s, int row) {
+      if (lane == 0 && ok) {
+        mbar_arrive_expect_tx(&q_full[qb], static_cast<uint32_t>(p.tok * p.GB * kD * 2));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          tma_3d(sq + (2 * qb + hf) * p.q_half, &mq, 64 * hf, s.h * p.G + s.chunk * kTile, row, &q_full[qb]);
+      }
+      __syncwarp();
+    };
+    for_segments([&](const Segment &s, uint32_t k) {
+      if constexpr (kPaged) {
+        const int qb = k & 1;
+        if (k >= 2) ok = ok && warp_wait(&q_free[qb], ((k >> 1) + 1) & 1u, p, abort);
+        load_q(qb, s, s.b * p.nq + s.row0);
+        const int end = none_sees(s);
+        const int box = min(kTile, 1 << p.ps_shift), boxes = kTile / box;
+        // lane 2 i + hf loads half hf of the tile's i-th page
+        const int hf = lane & 1, part = lane >> 1;
+        auto page_of = [&](int i) {  // row of this lane's part of tile i: -1 if nothing of it is seen
+          const int t = (s.j0 + i) * kTile + part * box;
+          if (i >= s.n[0] || part >= boxes || t >= end) return -1;
+          const int page = p.page_table[static_cast<int64_t>(s.b) * p.max_pages + (t >> p.ps_shift)];
+          return page < 0 || page >= p.num_pages ? -2 : page;
+        };
+        int pages[3] = {-1, -1, -1};  // of tiles i, i - 1, i - 2
+        int ahead = page_of(0);
+        for (int i = 0; i < s.n[0] + 2 && ok; ++i) {
+          pages[2] = pages[1];
+          pages[1] = pages[0];
+          pages[0] = ahead;
+          ahead = page_of(i + 1);
+          if (pages[0] == -2) {
+            set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
+            pages[0] = 0;
+          }
+          auto load = [&](int page, int tile, int kv) {
+            const uint32_t sl = next_slot();
+            if (!ok) return;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128u;
+            if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
+            __syncwarp();
+            if (page >= 0) {
+              const int off = ((s.j0 + tile) * kTile + part * box) & ((1 << p.ps_shift) - 1);
+              // one row per token: below 2^31 rows, checked on the host
+              const int row = ((page * 2 + kv) * p.H + s.h) * (1 << p.ps_shift) + off;
+              tma_2d(sr + sl * kTileBytes + hf * (kTileBytes / 2) + part * box * 128, &mk, 64 * hf, row, &full[sl]);
+            }
+            __syncwarp();
+          };
+          if (i >= 2 && i - 2 < s.n[0]) load(pages[2], i - 2, 1);
+          if (i < s.n[0]) load(pages[0], i, 0);
+        }
+      } else {
+        if (s.n[0]) load_q(0, s, s.kv0 + s.row0);
+        const int n = max(s.n[0], s.n[1]);
+        for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t sl = next_slot();
+            if (lane == 0 && ok) {
+              mbar_arrive_expect_tx(&full[sl], kTileBytes);
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile,
+                       &full[sl]);
+            }
+            __syncwarp();
+            if (j == 0 && kv == 0 && s.n[1]) load_q(1, s, s.kv0 + s.row0 + p.tok);
+          }
+        }
+      }
+      return ok;
+    });
+    if (!ok) {
+      // copies may be in flight: wait for those of every slot's last use
+      for (uint32_t i = 0; i < static_cast<uint32_t>(p.slots); ++i) {
+        const uint32_t used = round + (i < slot ? 1u : 0u);
+        if (used > 0) mbar_wait(&full[i], (used - 1) & 1u, p.status, nullptr);
+      }
+    }
+  } else if (warp >= kGuardWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // --------------------------------------------------------------- guards
+    uint32_t slot = 0, round = 0, n_clear = 0, n_go = 0;
+    bool ok = true;
+    const int g = tid - kGuardWarp * 32;
+    for_segments([&](const Segment &s, uint32_t k) {
+      const int all = all_see(s), none_after = none_sees(s);
+      const int n = kPaged ? s.n[0] : max(s.n[0], s.n[1]);
+      bool fresh = k > 0;
+      // the order of use: K0 K1 V0 K2 V1 .. (cache), K0 V0 K1 V1 .. (prompts)
+      auto visit = [&](int tile, bool is_v) {
+        const uint32_t sl = slot, rd = round;
+        if (++slot == static_cast<uint32_t>(p.slots)) {
+          slot = 0;
+          ++round;
+        }
+        const int t0 = (s.j0 + tile) * kTile;
+        if (!is_v || t0 + kTile <= all || !ok) return;
+        // The MMA warp has the tile: the phases that the waits below name are
+        // those of this tile and of the segment before.
+        ok = warp_wait(guard_go, n_go & 1u, p, abort);
+        ++n_go;
+        if (fresh) {
+          // the marks of the segment before are read no more
+          ok = ok && warp_wait(seg_done, (k - 1) & 1u, p, abort);
+          fresh = false;
+          if (warp == kGuardWarp) {
+            if (*nonfinite) {
+              for (int i = lane; i < 3 * kD; i += 32) bad[i] = INT_MAX;
+              __syncwarp();
+              if (lane == 0) *nonfinite = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cleared);
+          } else {
+            ok = ok && warp_wait(cleared, n_clear & 1u, p, abort);
+          }
+          ++n_clear;
+        }
+        ok = ok && warp_wait(&full[sl], rd & 1u, p, abort);
+        uint8_t *tile_v = ring + sl * kTileBytes;
+        const uint32_t mask = exponent_mask<T>();
+        for (int r = max(0, all - t0) + (g >> 4); r < kTile; r += 4) {
+          const int chunk = g & 15;  // 16-byte chunk: half chunk / 8, swizzled by the row
+          uint4 *at = reinterpret_cast<uint4 *>(tile_v + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (chunk & 7) * 16);
+          if (t0 + r >= none_after) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
+          uint4 v = *at;
+          uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
+          if (any) {
+            const int dim0 = (chunk >> 3) * 64 + (((chunk & 7) ^ (r & 7)) * 8);
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu, m = mask & 0xffffu;
+              if ((x & m) != m) continue;
+              const int kind = (x & 0x7fffu) != m ? 2 : (x >> 15);
+              atomicMin(&bad[kind * kD + dim0 + e], t0 + r);
+              w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+            }
+            *nonfinite = 1;
+            *at = v;
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(guarded);
+      };
+      if constexpr (kPaged) {
+        for (int i = 0; i < n + 2; ++i) {
+          if (i >= 2 && i - 2 < n) visit(i - 2, true);
+          if (i < n) visit(i, false);
+        }
+      } else {
+        for (int j = 0; j < n; ++j) {
+          visit(j, false);
+          visit(j, true);
+        }
+      }
+      return ok;
+    });
+  } else {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = warp >> 2, r = tid & (kTile - 1);
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
+    const int r_tok = r / p.GB, r_head = r - r_tok * p.GB;
+    uint32_t n_s = 0, n_o1 = 0;
+    bool ok = true;
+    // one row's sum of products, times f, plus what the guards took out
+    auto finish = [&](const Segment &s, int lim, float (&o)[32], int col, float f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] *= f;
+      if (*nonfinite) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (bad[col + i] < lim) o[i] += INFINITY;
+          if (bad[kD + col + i] < lim) o[i] -= INFINITY;
+          if (bad[2 * kD + col + i] < lim) o[i] = NAN;
+        }
+      }
+    };
+    auto store16 = [&](T *dst, const float (&o)[32]) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        *reinterpret_cast<uint4 *>(dst + i) =
+            make_uint4(pack16(o[i], o[i + 1], T()), pack16(o[i + 2], o[i + 3], T()), pack16(o[i + 4], o[i + 5], T()),
+                       pack16(o[i + 6], o[i + 7], T()));
+    };
+    if ((warp & 3) < row_warps) for_segments([&](const Segment &s, uint32_t k) {
+      const int n = kPaged ? (s.n[0] + 1 - x) >> 1 : s.n[x];
+      const int qi = s.row0 + (kPaged ? 0 : x * p.tok) + r_tok;
+      const int hq = s.chunk * kTile + r_head;
+      const bool valid = r < p.R && qi < s.rows && hq < p.G;
+      const int lim = valid ? s.limit(qi, p.causal) : 0;
+      float ref = -INFINITY, l = 0.f;
+      for (int i = 0; i < n && ok; ++i) {
+        const int t0 = (s.j0 + (kPaged ? 2 * i + x : i)) * kTile;
+        ok = warp_wait(&s_full[x], n_s & 1u, p, abort);
+        ++n_s;
+        // Side 1's O and sums are merged by side 0 before it writes them again.
+        // (Its scores are here, so side 0 is past segment k - 2 and the parity
+        // is that of k - 1.)
+        if (kPaged && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(seg_done, (k - 1) & 1u, p, abort);
+        if (!ok) break;
+        tc_fence_after();
+        softmax_tile<T, kLo>(ts, to, p.c, lim - t0, i == 0, ref, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) return false;
+      const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
+      if constexpr (!kPaged) {
+        if (n == 0) return true;
+        ok = warp_wait(&o_done[x], 0, p, abort);
+        if (!ok) return false;
+        tc_fence_after();
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        T *dst = static_cast<T *>(p.out) +
+                 (static_cast<int64_t>(s.kv0 + qi) * p.Hq + static_cast<int64_t>(s.h) * p.G + hq) * kD;
+#pragma unroll
+        for (int col = 0; col < kD; col += 32) {
+          float o[32];
+          tmem_ld32(to + col, o);
+          finish(s, lim, o, col, inv);
+          if (valid) store16(dst + col, o);
+        }
+      } else if (x == 1) {
+        if (n > 0) {
+          ml[r] = make_float2(sub, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(side1);
+        }
+      } else {
+        const bool both = s.n[0] > 1;
+        ok = warp_wait(&o_done[0], k & 1u, p, abort);
+        if (both) {
+          ok = ok && warp_wait(&o_done[1], n_o1 & 1u, p, abort) && warp_wait(side1, n_o1 & 1u, p, abort);
+          ++n_o1;
+        }
+        if (!ok) return false;
+        tc_fence_after();
+        float m = sub, w0 = 1.f, w1 = 0.f;
+        if (both) {
+          const float2 other = ml[r];
+          // a NaN reference weighs NaN
+          m = fmaxf(sub, other.x);
+          const float base = m == -INFINITY ? 0.f : m;
+          w0 = ex2f(sub - base);
+          w1 = ex2f(other.x - base);
+          l = l * w0 + other.y * w1;
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        // whole: the result; else a record for the combine kernel
+        float *rec = p.records + (static_cast<int64_t>(2) * blockIdx.x + (s.starts ? 1 : 0)) *
+                                     (static_cast<int64_t>(p.row_stride) * (kD + 2));
+        T *dst = static_cast<T *>(p.out) + ((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq +
+                                            static_cast<int64_t>(s.h) * p.G + hq) * kD;
+        if (valid && !s.whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
+#pragma unroll
+        for (int col = 0; col < kD; col += 32) {
+          float o[32];
+          tmem_ld32(to + col, o);
+          if (both) {
+            float o1[32];
+            tmem_ld32(to + 128 + col, o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+          }
+          finish(s, lim, o, col, s.whole ? inv : 1.f);
+          if (valid) {
+            if (s.whole) {
+              store16(dst + col, o);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(rec + 2 * p.row_stride + r * kD + col + i) =
+                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_done);
+      }
+      return true;
+    });
+  }
+  if constexpr (kPaged) {
+    // the segment that starts here and goes on in the CTAs behind, for the combine kernel
+    if (tid == 0) {
+      const int64_t gs = my_loc[0], ge = my_loc[1], total = my_loc[4];
+      int2 plan = make_int2(-1, 0);
+      if (gs < ge) {
+        Walk16 wk(p, my_loc);
+        Segment s;
+        while (wk.next(p, s)) {
+          if (s.starts && !s.whole) {
+            const int64_t N = min(static_cast<int64_t>(p.n_cta), total);
+            const int64_t last = ge + (wk.un.nt - wk.j) - 1;  // the segment's last tile
+            plan = make_int2(s.id, static_cast<int>(((last + 1) * N + total - 1) / total - 1));
+          }
+        }
+      }
+      p.plan[blockIdx.x] = plan;
+    }
+  }
+  // the products must complete before tensor memory is released
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    if (*issued) mbar_wait(mma_done, 0, p.status, nullptr);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// Joins the records of each segment that spans CTAs: block (c, y) the rows 4 y
+// .. of the one that starts in CTA c and goes on, one warp per row.  Record
+// 2 c + 1 holds its first part, 2 k those of the CTAs k behind.
+template <typename T>
+__global__ void __launch_bounds__(128) k_combine16(const Attend16 p) {
+  pdl_trigger();
+  pdl_wait();
+  const int2 plan = p.plan[blockIdx.x];
+  if (plan.x < 0) return;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int u = plan.x / p.H, h = plan.x - u * p.H;
+  const int rts = (p.nq + p.tok - 1) / p.tok * p.chunks;
+  const int b = u / rts, rt = u - b * rts;
+  const int qi = rt / p.chunks * p.tok + r / p.GB, hq = rt % p.chunks * kTile + r % p.GB;
+  if (r >= p.R || qi >= p.nq || hq >= p.G) return;
+  const int64_t size = static_cast<int64_t>(p.row_stride) * (kD + 2);
+  const int first = blockIdx.x, count = plan.y - first + 1;
+  auto rec = [&](int i) { return p.records + (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * size; };
+  float m = -INFINITY;
+  for (int i = lane; i < count; i += 32) m = fmaxf(m, rec(i)[2 * r]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < count) {
+      const float2 t = *reinterpret_cast<const float2 *>(rec(i0 + lane) + 2 * r);
+      w = ex2f(t.x - base);
+      l += w * t.y;
+    }
+    const int top = min(32, count - i0);
+#pragma unroll 8
+    for (int i = 0; i < top; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float4 o = *reinterpret_cast<const float4 *>(rec(i0 + i) + 2 * p.row_stride + r * kD + 4 * lane);
+      acc.x = fmaf(wi, o.x, acc.x); acc.y = fmaf(wi, o.y, acc.y);
+      acc.z = fmaf(wi, o.z, acc.z); acc.w = fmaf(wi, o.w, acc.w);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  T *dst = static_cast<T *>(p.out) +
+           ((static_cast<int64_t>(b) * p.nq + qi) * p.Hq + static_cast<int64_t>(h) * p.G + hq) * kD + 4 * lane;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack16(acc.x * inv, acc.y * inv, T()), pack16(acc.z * inv, acc.w * inv, T()));
+}
+
+// --------------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's encoder, looked up once
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void *sym = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeFn>(nullptr);
+    return reinterpret_cast<EncodeFn>(sym);
+  }();
+  return fn;
+}
+
+// 64-dim boxes with the 128-byte swizzle
+bool encode(CUtensorMap *map, int dtype, int rank, const void *base, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const EncodeFn fn = encoder();
+  return fn != nullptr &&
+         fn(map, dtype == ISOQUANT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+            const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [tokens][heads][128], tokens `stride` elements apart; box_heads x box_tokens
+bool encode_rows(CUtensorMap *map, int dtype, const void *base, int64_t tokens, int heads, int64_t stride,
+                 int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  return encode(map, dtype, 3, base, dims, strides, box);
+}
+
+void row_tiles(Attend16 &p, int group) {
+  p.G = group;
+  p.GB = group < kTile ? group : kTile;
+  p.chunks = (group + kTile - 1) / kTile;
+  p.tok = kTile / p.GB;
+}
+
+template <typename T, bool kPaged>
+cudaError_t launch16(const Attend16 &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                     unsigned grid, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(4) * p.q_half + static_cast<size_t>(p.slots) * kTileBytes + kTailBytes;
+  const cudaError_t e = cudaFuncSetAttribute(k_attend16<T, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_attend16<T, kPaged>, dim3(grid), dim3(kThreads16), smem, stream, p, mq, mk, mv);
+}
+
+// the cache's row tiles: rows, and the stride of a record's rows
+void paged_rows(Attend16 &p, const AttendShape &s) {
+  row_tiles(p, s.group);
+  if (p.tok > s.nq) p.tok = s.nq;
+  p.R = p.tok * p.GB;
+  p.row_stride = (p.R + 1) / 2 * 2;
+}
+
+size_t plan_bytes(int n_cta) { return (static_cast<size_t>(n_cta) * sizeof(int2) + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const void *k, const void *v, int dtype,
+                                 int n_tok, int num_q_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 const int32_t *cu_seqlens, int batch, int causal, float scale, void *out,
+                                 cudaStream_t stream) {
+  Attend16 p{};
+  p.H = ctx->num_kv_heads;
+  p.Hq = num_q_heads;
+  row_tiles(p, p.Hq / p.H);
+  p.R = p.tok * p.GB;
+  p.B = batch;
+  p.causal = causal;
+  p.c = scale * 1.4426950408889634f;
+  p.cu = cu_seqlens;
+  p.n_tok = n_tok;
+  p.slots = 5;
+  p.q_half = kTileBytes / 2;
+  p.out = out;
+  p.status = ctx->status;
+  CUtensorMap mq, mk, mv;
+  if (!encode_rows(&mq, dtype, q, n_tok, p.Hq, q_stride, p.GB, p.tok) ||
+      !encode_rows(&mk, dtype, k, n_tok, p.H, k_stride, 1, kTile) ||
+      !encode_rows(&mv, dtype, v, n_tok, p.H, v_stride, 1, kTile))
+    return cudaErrorInvalidValue;
+  // pairs of row tiles: no more than one per 2 tok tokens and one per sequence
+  const int64_t grid = (static_cast<int64_t>(n_tok) / (2 * p.tok) + batch) * p.H;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return dtype == ISOQUANT_BF16
+             ? launch16<__nv_bfloat16, false>(p, mq, mk, mv, static_cast<unsigned>(grid), stream)
+             : launch16<__half, false>(p, mq, mk, mv, static_cast<unsigned>(grid), stream);
+}
+
+size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s) {
+  Attend16 p{};
+  paged_rows(p, s);
+  return plan_bytes(ctx->num_sms) +
+         static_cast<size_t>(2) * ctx->num_sms * p.row_stride * (kD + 2) * sizeof(float);
+}
+
+cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const AttendShape &s,
+                                const void *q, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
+                                float scale, void *ws, void *out, cudaStream_t stream) {
+  Attend16 p{};
+  p.H = s.kv_heads;
+  p.Hq = s.q_heads;
+  paged_rows(p, s);
+  p.B = s.batch;
+  p.nq = s.nq;
+  p.causal = s.causal;
+  p.c = scale * 1.4426950408889634f;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.max_pages = max_pages;
+  p.num_pages = cache->num_pages;
+  while ((1 << p.ps_shift) < cache->page_size) ++p.ps_shift;
+  p.n_cta = ctx->num_sms;
+  p.plan = static_cast<int2 *>(ws);
+  p.records = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(p.n_cta));
+  // up to 64 rows a Q buffer's halves need 64 rows each, which leaves room for another slot
+  p.slots = p.R <= kTile / 2 ? 6 : 5;
+  p.q_half = p.R <= kTile / 2 ? kTileBytes / 4 : kTileBytes / 2;
+  p.out = out;
+  p.status = ctx->status;
+  CUtensorMap mq, mk;
+  const int64_t rows = static_cast<int64_t>(cache->num_pages) * 2 * p.H * cache->page_size;
+  const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {kD * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(cache->page_size < kTile ? cache->page_size : kTile)};
+  if (!encode_rows(&mq, cache->dtype, q, static_cast<int64_t>(s.batch) * s.nq, p.Hq,
+                   static_cast<int64_t>(p.Hq) * kD, p.GB, p.tok) ||
+      !encode(&mk, cache->dtype, 2, cache->data, dims, strides, box))
+    return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(p.n_cta);
+  const bool bf = cache->dtype == ISOQUANT_BF16;
+  const cudaError_t e = bf ? launch16<__nv_bfloat16, true>(p, mq, mk, mk, grid, stream)
+                           : launch16<__half, true>(p, mq, mk, mk, grid, stream);
+  if (e != cudaSuccess) return e;
+  const dim3 cg(grid, static_cast<unsigned>((p.R + 3) / 4)), block(128);
+  return bf ? launch_pdl(k_combine16<__nv_bfloat16>, cg, block, 0, stream, p)
+            : launch_pdl(k_combine16<__half>, cg, block, 0, stream, p);
+}
+
+}  // namespace isoquant

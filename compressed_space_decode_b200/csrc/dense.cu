@@ -1,6 +1,5 @@
-// dense.cu -- the paged cache of 16-bit keys and values: isoquant_dense_prep
-// (append with the position rotation) and isoquant_dense_attend (attention of
-// the newest tokens, split over the context and joined).
+// dense.cu -- isoquant_dense_prep: appends to the paged cache of 16-bit keys
+// and values, with the position rotation of keys and queries.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -160,59 +159,6 @@ __global__ void __launch_bounds__(256) k_dense_prep(const DensePrepArgs g) {
   }
 }
 
-// --------------------------------------------------------------- attention
-struct DenseArgs {
-  const void *data, *q;
-  void *out;
-  const int32_t *page_table, *seq_lens;
-  int max_pages, num_pages, ps_shift;
-  int B, nq, Hq, H, G, causal;
-  float scale;
-  uint32_t *status;
-};
-
-// One warp per output row, four coordinates per lane, the running maximum and
-// sum of the softmax in fp32.
-template <typename T>
-__global__ void __launch_bounds__(256) k_dense_rows(const DenseArgs p) {
-  pdl_trigger();
-  pdl_wait();
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<int64_t>(p.B) * p.nq * p.Hq) return;
-  const int hq = static_cast<int>(w % p.Hq), i = static_cast<int>(w / p.Hq % p.nq);
-  const int b = static_cast<int>(w / p.Hq / p.nq), h = hq / p.G;
-  const int L = p.seq_lens[b], ps = 1 << p.ps_shift;
-  const int limit = p.causal ? L - p.nq + i + 1 : L;
-  const uint2 qw = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.q) + w * kD + 4 * lane);
-  const float2 q0 = unpack2(qw.x, T()), q1 = unpack2(qw.y, T());
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t = 0; t < limit; ++t) {
-    int page = t >> p.ps_shift < p.max_pages ? p.page_table[static_cast<int64_t>(b) * p.max_pages + (t >> p.ps_shift)] : -1;
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
-      page = 0;
-    }
-    const T *k = static_cast<const T *>(p.data) +
-                 ((static_cast<int64_t>(page) * 2 * p.H + h) * ps + (t & (ps - 1))) * kD + 4 * lane;
-    const uint2 kw = *reinterpret_cast<const uint2 *>(k);
-    const uint2 vw = *reinterpret_cast<const uint2 *>(k + static_cast<int64_t>(p.H) * ps * kD);
-    const float2 k0 = unpack2(kw.x, T()), k1 = unpack2(kw.y, T()), v0 = unpack2(vw.x, T()), v1 = unpack2(vw.y, T());
-    float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), a = __expf(m - mn), e = __expf(s - mn);
-    m = mn;
-    l = l * a + e;
-    o[0] = o[0] * a + e * v0.x; o[1] = o[1] * a + e * v0.y;
-    o[2] = o[2] * a + e * v1.x; o[3] = o[3] * a + e * v1.y;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + w * kD + 4 * lane) =
-      make_uint2(pack2(o[0] * inv, o[1] * inv, T()), pack2(o[2] * inv, o[3] * inv, T()));
-}
-
 int shift_of(int page_size) {
   int s = 0;
   while ((1 << s) < page_size) ++s;
@@ -253,24 +199,6 @@ cudaError_t launch_dense_prep(const isoquant_ctx *ctx, const isoquant_dense_cach
                    : launch_pdl(k_dense_prep<__nv_bfloat16, 1>, grid, block, 0, stream, g);
   return hc == 4 ? launch_pdl(k_dense_prep<__half, 4>, grid, block, 0, stream, g)
                  : launch_pdl(k_dense_prep<__half, 1>, grid, block, 0, stream, g);
-}
-
-size_t dense_workspace_bytes(const AttendShape &s) { return kWsHeader; }
-
-cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const AttendShape &s,
-                                const void *q, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
-                                float scale, void *ws, void *out, cudaStream_t stream) {
-  DenseArgs p{};
-  p.data = cache->data; p.q = q; p.out = out;
-  p.page_table = page_table; p.seq_lens = seq_lens;
-  p.max_pages = max_pages; p.num_pages = cache->num_pages; p.ps_shift = shift_of(cache->page_size);
-  p.B = s.batch; p.nq = s.nq; p.Hq = s.q_heads; p.H = s.kv_heads; p.G = s.group; p.causal = s.causal;
-  p.scale = scale;
-  p.status = ctx->status;
-  const int64_t rows = static_cast<int64_t>(s.batch) * s.nq * s.q_heads;
-  const dim3 grid(static_cast<unsigned>((rows + 7) / 8)), block(256);
-  return cache->dtype == ISOQUANT_BF16 ? launch_pdl(k_dense_rows<__nv_bfloat16>, grid, block, 0, stream, p)
-                                       : launch_pdl(k_dense_rows<__half>, grid, block, 0, stream, p);
 }
 
 }  // namespace isoquant

@@ -77,7 +77,7 @@ cudaError_t launch_decode_prep_rope(const isoquant_ctx *ctx, const isoquant_cach
                                     const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
                                     const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
                                     const isoquant_rope *rope, float *q_rot, cudaStream_t stream);
-// 16-bit cache and prompt attention (dense.cu, prompt.cu)
+// 16-bit cache and prompt attention (dense.cu, attend16.cu)
 cudaError_t launch_dense_prep(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const void *k,
                               const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
                               const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
@@ -110,7 +110,7 @@ cudaError_t launch_attend_partial(const isoquant_ctx *ctx, const isoquant_cache 
 cudaError_t launch_attend_combine(const isoquant_ctx *ctx, const AttendShape &s,
                                   const int32_t *seq_lens, const void *ws, size_t ws_bytes, float *out,
                                   cudaStream_t stream);
-size_t dense_workspace_bytes(const AttendShape &s);
+size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s);
 cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_cache *cache, const AttendShape &s,
                                 const void *q, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
                                 float scale, void *ws, void *out, cudaStream_t stream);

@@ -319,8 +319,11 @@ int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq,
  *   workspace: device, >= isoquant_dense_workspace_size bytes, 16-byte
  *        aligned; its contents on entry do not matter; calls whose kernels
  *        overlap on the GPU must not share one workspace
- * A row that sees no token outputs zeros.  Two kernel launches.  Errors:
- * INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
+ * A row that sees no token, or only keys whose scores are -inf, outputs
+ * zeros; a NaN score makes its row NaN.  A length beyond the page table's
+ * max_pages pages sets ISOQUANT_DEVERR_PAGE_RANGE and counts as their tokens.
+ * Two kernel launches.  Errors: INVALID_ARG (also more than 2^31 - 1 cached
+ * vectors), UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
                           const void *q, int batch, int nq, int num_q_heads,
                           const int32_t *page_table, int max_pages,
@@ -337,14 +340,14 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
  *      heads' extent), 16-byte aligned
  *   cu_seqlens: device int32 [batch + 1]: sequence b is tokens
  *      cu_seqlens[b] .. cu_seqlens[b + 1] - 1; empty ones are allowed.
- *      Entries that decrease or leave [0, n_tok] set
- *      ISOQUANT_DEVERR_SEQ_RANGE and that sequence is skipped
+ *      A sequence whose entries decrease, leave [0, n_tok] or lie below an
+ *      earlier entry sets ISOQUANT_DEVERR_SEQ_RANGE and is skipped
  *   causal: if nonzero, a token sees itself and the tokens before it in its
  *      sequence, otherwise its whole sequence
  *   scale: softmax scale; 0 selects 1/sqrt(128)
  *   out: device [n_tok][num_q_heads][128] of `dtype`, contiguous, 16-byte
  *      aligned, apart from the inputs; rows of no sequence are left as they
- *      were
+ *      were (a row whose every score is -inf outputs zeros)
  * Scores, softmax statistics and sums in fp32; softmax weights are rounded
  * to `dtype` for the product with v.  One kernel launch, no workspace.
  * num_q_heads / num_kv_heads at most 128.  Errors: INVALID_ARG, UNSUPPORTED
