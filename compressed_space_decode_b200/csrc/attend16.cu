@@ -48,13 +48,13 @@ constexpr int kTileBytes = kTile * kD * 2;  // 32 KB
 constexpr int kThreads16 = 3 * 128;         // two sides, then the MMA, loader and two guard warps
 constexpr int kMaxSlots = 6;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10;
-// shared memory: the tiles, then
-constexpr int kOffBad = 0;                        // first token with +inf, -inf, NaN of each dim
-constexpr int kOffMl = kOffBad + 3 * kD * 4;      // side 1's (reference, sum) of each row; first the locate scratch
-constexpr int kOffBar = kOffMl + kTile * 8;       // barriers
-constexpr int kNumBars = 2 * kMaxSlots + 2 + 2 + 2 + 2 + 2 + 6;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tensor-memory base, abort flag, MMA-issued flag, non-finite flag
-constexpr int kTailBytes = kOffMisc + 16;
+// shared memory behind the tiles
+constexpr int kOffBad = 0;                      // first token with +inf, -inf, NaN of each dim
+constexpr int kOffBar = kOffBad + 3 * kD * 4;   // barriers
+constexpr int kOffFlags = kOffBar + 256;
+constexpr int kOffLoc = kOffFlags + 16;         // the CTA's part, then locate's scratch
+constexpr int kTailBytes = kOffLoc + 160;
+constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (reference, sum) of each row
 
 struct Attend16 {
   int H, Hq, G, GB, chunks, tok, R, B, nq, causal;  // GB: heads of a row tile (G, or 128 of a larger group)
@@ -91,17 +91,33 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, __half) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ __nv_bfloat16 to16(float x, __nv_bfloat16) { return __float2bfloat16_rn(x); }
+__device__ __forceinline__ __half to16(float x, __half) { return __float2half_rn(x); }
+// A sum without the non-finite values that guard_tile took out of dim d: with
+// those that a row seeing `lim` tokens sees.
+__device__ __forceinline__ float with_nonfinite(float o, const int *bad, int d, int lim) {
+  if (bad[d] < lim) o += INFINITY;
+  if (bad[kD + d] < lim) o -= INFINITY;
+  return bad[2 * kD + d] < lim ? NAN : o;
+}
+
 // shared-memory matrix descriptor, 128-byte swizzle, strides in 16-byte units
 __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo) << 16) |
          (static_cast<uint64_t>(sbo) << 32) | (1ull << 46) | (2ull << 61);
 }
-// A, B of type T (bf16 or fp16, both the same), fp32 accumulator, 128 x 128
+// no swizzle: 8 x 16-byte pieces, `lbo` and `sbo` units apart along the two axes
+__device__ __forceinline__ uint64_t desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo) << 16) |
+         (static_cast<uint64_t>(sbo) << 32) | (1ull << 46);
+}
+// A, B of type T (bf16 or fp16, both the same), fp32 accumulator, 128 x n;
+// mn: the operand's 16-bit elements run along M or N, not K
 template <typename T>
-__device__ constexpr uint32_t idesc16(int b_mn_major) {
-  constexpr uint32_t t = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(b_mn_major) << 16) | ((128u >> 3) << 17) |
-         ((128u >> 4) << 24);
+__device__ constexpr uint32_t idesc16(int n, int a_mn, int b_mn) {
+  constexpr uint32_t t = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -398,36 +414,13 @@ __device__ __forceinline__ uint32_t exponent_mask() {
   return std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
 }
 
-// kPaged: the cache's form, else prompts.  kLo: bf16 weights as two operands
-// (16 bits), so that the result is off by one rounding.
-template <typename T, bool kPaged>
-__global__ void __launch_bounds__(kThreads16, 1)
-    k_attend16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv) {
-  constexpr bool kLo = kPaged && std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t *ring = smem + 4 * p.q_half, *tail = ring + p.slots * kTileBytes;
-  int *bad = reinterpret_cast<int *>(tail + kOffBad);
-  float2 *ml = reinterpret_cast<float2 *>(tail + kOffMl);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(tail + kOffBar);
-  uint64_t *full = bars, *freed = bars + kMaxSlots, *q_full = bars + 2 * kMaxSlots, *q_free = q_full + 2,
-           *s_full = q_full + 4, *p_full = q_full + 6, *o_done = q_full + 8, *guarded = q_full + 10,
-           *side1 = guarded + 1, *seg_done = guarded + 2, *mma_done = guarded + 3, *cleared = guarded + 4, *guard_go = guarded + 5;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + kOffMisc);
-  volatile int *abort = reinterpret_cast<volatile int *>(tail + kOffMisc + 4);
-  volatile int *issued = reinterpret_cast<volatile int *>(tail + kOffMisc + 8);
-  volatile int *nonfinite = reinterpret_cast<volatile int *>(tail + kOffMisc + 12);
-  int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffMl);
-  const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
-
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
-                 "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
-    tc_fence_before();
-  }
-  if (tid == 32) {
+// The barriers of a CTA: ring slots filled and freed, queries there and used,
+// a side's scores, weights and last product, then the guards' (guarded, go,
+// cleared) and the sides' hand-overs.
+struct Bars {
+  uint64_t full[kMaxSlots], freed[kMaxSlots], q_full[2], q_free[2], s_full[2], p_full[2], o_done[2];
+  uint64_t guarded, go, cleared, side1, seg_done, mma_done;
+  __device__ void init(int p_count, int seg_count) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&freed[i], 1);
@@ -436,56 +429,294 @@ __global__ void __launch_bounds__(kThreads16, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], row_warps);
+      mbar_init(&p_full[i], p_count);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(guarded, 2);
-    mbar_init(side1, row_warps);
-    mbar_init(seg_done, row_warps);
-    mbar_init(mma_done, 1);
-    mbar_init(cleared, 1);
-    mbar_init(guard_go, 1);
-    *abort = 0;
-    *issued = 0;
-    *nonfinite = 0;
+    mbar_init(&guarded, 2);
+    mbar_init(&go, 1);
+    mbar_init(&cleared, 1);
+    mbar_init(&side1, seg_count);
+    mbar_init(&seg_done, seg_count);
+    mbar_init(&mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < 3 * kD; i += kThreads16) bad[i] = INT_MAX;
+};
+static_assert(sizeof(Bars) <= 256, "room for the barriers");
+// what the roles of a CTA share beside the barriers
+struct Flags {
+  uint32_t tmem;
+  int abort, issued, nonfinite;
+};
+
+// the next ring slot in the order of use, and how often it was used before
+struct Ring {
+  uint32_t slot = 0, round = 0;
+  int slots;
+  __device__ explicit Ring(int n) : slots(n) {}
+  __device__ uint32_t step() {
+    const uint32_t s = slot;
+    if (++slot == static_cast<uint32_t>(slots)) {
+      slot = 0;
+      ++round;
+    }
+    return s;
+  }
+};
+
+__device__ __forceinline__ float *record(const Attend16 &p, int i) {
+  return p.records + i * (static_cast<int64_t>(p.row_stride) * (kD + 2));
+}
+
+// Tensor memory of COLS columns, the barriers and the guards' marks; the
+// caller's next __syncthreads makes them visible.
+template <uint32_t COLS>
+__device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, int p_count, int seg_count) {
+  if (threadIdx.x < 32) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&flags->tmem)),
+                 "r"(COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+    tc_fence_before();
+  }
+  if (threadIdx.x == 32) {
+    bars.init(p_count, seg_count);
+    flags->abort = flags->issued = flags->nonfinite = 0;
+  }
+  for (int i = threadIdx.x; i < 3 * kD; i += kThreads16) bad[i] = INT_MAX;
+}
+// the products must complete before tensor memory is released
+template <uint32_t COLS>
+__device__ __forceinline__ void end_cta(Bars &bars, Flags *flags, const Attend16 &p) {
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    if (*const_cast<volatile int *>(&flags->issued)) mbar_wait(&bars.mma_done, 0, p.status, nullptr);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(flags->tmem), "r"(COLS));
+  }
+}
+
+// f(segment, number) for each segment of the CTA's part, until f says stop
+template <typename F>
+__device__ __forceinline__ void cache_segments(const Attend16 &p, const int64_t *loc, F &&f) {
+  Walk16 wk(p, loc);
+  Segment s;
+  for (uint32_t k = 0; wk.next(p, s); ++k)
+    if (!f(s, k)) return;
+}
+// the token below which every row of the segment sees all, and the first that none sees
+__device__ __forceinline__ int all_see(const Attend16 &p, const Segment &s) { return s.limit(s.row0, p.causal); }
+__device__ __forceinline__ int none_sees(const Attend16 &p, const Segment &s, int tokens) {
+  return s.limit(min(s.rows, s.row0 + tokens) - 1, p.causal);
+}
+
+// Before a CTA that gave up ends: waits for the copies of each slot's last use.
+__device__ void drain(const Attend16 &p, const Ring &ring, Bars &bars, bool ok) {
+  if (ok) return;
+  for (uint32_t i = 0; i < static_cast<uint32_t>(p.slots); ++i) {
+    const uint32_t used = ring.round + (i < ring.slot ? 1u : 0u);
+    if (used > 0) mbar_wait(&bars.full[i], (used - 1) & 1u, p.status, nullptr);
+  }
+}
+
+// The loader warp over the cache: key and value tiles in the order of their
+// use, K0 K1 V0 K2 V1 .., and the segments' queries into q_bufs buffers whose
+// 64-dim halves are p.q_half bytes.
+__device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensorMap &mq, const CUtensorMap &mk,
+                           uint32_t sq, uint32_t sr, int q_bufs, Bars &bars, volatile int *abort) {
+  const int lane = threadIdx.x & 31;
+  Ring ring(p.slots);
+  bool ok = true;
+  cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
+    const uint32_t qb = k % q_bufs, use = k / q_bufs;
+    if (use > 0) ok = ok && warp_wait(&bars.q_free[qb], (use - 1) & 1u, p, abort);
+    if (lane == 0 && ok) {
+      mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(p.R * kD * 2));
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        tma_3d(sq + (2 * qb + hf) * p.q_half, &mq, 64 * hf, s.h * p.G + s.chunk * kTile, s.b * p.nq + s.row0,
+               &bars.q_full[qb]);
+    }
+    __syncwarp();
+    const int end = none_sees(p, s, p.tok);
+    const int box = min(kTile, 1 << p.ps_shift), boxes = kTile / box;
+    // lane 2 i + hf loads half hf of the tile's i-th page
+    const int hf = lane & 1, part = lane >> 1;
+    auto page_of = [&](int i) {  // this lane's page of tile i: -1 if nothing of it is seen, -2 if it is none
+      const int t = (s.j0 + i) * kTile + part * box;
+      if (i >= s.n[0] || part >= boxes || t >= end) return -1;
+      const int page = p.page_table[static_cast<int64_t>(s.b) * p.max_pages + (t >> p.ps_shift)];
+      return page < 0 || page >= p.num_pages ? -2 : page;
+    };
+    int pages[3] = {-1, -1, -1};  // of tiles i, i - 1, i - 2
+    int ahead = page_of(0);
+    for (int i = 0; i < s.n[0] + 2 && ok; ++i) {
+      pages[2] = pages[1];
+      pages[1] = pages[0];
+      pages[0] = ahead;
+      ahead = page_of(i + 1);
+      if (pages[0] == -2) {
+        set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
+        pages[0] = 0;
+      }
+      auto load = [&](int page, int tile, int kv) {
+        if (ring.round > 0) ok = ok && warp_wait(&bars.freed[ring.slot], (ring.round - 1) & 1u, p, abort);
+        if (!ok) return;
+        const uint32_t sl = ring.step();
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128u;
+        if (lane == 0) mbar_arrive_expect_tx(&bars.full[sl], bytes);
+        __syncwarp();
+        if (page >= 0) {
+          const int off = ((s.j0 + tile) * kTile + part * box) & ((1 << p.ps_shift) - 1);
+          // one row per token: below 2^31 rows, checked on the host
+          const int row = ((page * 2 + kv) * p.H + s.h) * (1 << p.ps_shift) + off;
+          tma_2d(sr + sl * kTileBytes + hf * (kTileBytes / 2) + part * box * 128, &mk, 64 * hf, row, &bars.full[sl]);
+        }
+        __syncwarp();
+      };
+      if (i >= 2 && i - 2 < s.n[0]) load(pages[2], i - 2, 1);
+      if (i < s.n[0]) load(pages[0], i, 0);
+    }
+    return ok;
+  });
+  drain(p, ring, bars, ok);
+}
+
+// One guard warp's share of a value tile (tokens from t0 on): rows that no
+// query row sees are cleared, non-finite elements of rows that some see are
+// taken out and their first token noted.
+template <typename T>
+__device__ void guard_tile(uint8_t *tile, int t0, int all, int none, int g, int *bad, volatile int *nonfinite) {
+  const uint32_t mask = exponent_mask<T>();
+  for (int r = max(0, all - t0) + (g >> 4); r < kTile; r += 4) {
+    const int chunk = g & 15;  // 16-byte chunk: half chunk / 8, swizzled by the row
+    uint4 *at = reinterpret_cast<uint4 *>(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (chunk & 7) * 16);
+    if (t0 + r >= none) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    uint4 v = *at;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
+    if (any) {
+      const int dim0 = (chunk >> 3) * 64 + (((chunk & 7) ^ (r & 7)) * 8);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu, m = mask & 0xffffu;
+        if ((x & m) != m) continue;
+        const int kind = (x & 0x7fffu) != m ? 2 : (x >> 15);
+        atomicMin(&bad[kind * kD + dim0 + e], t0 + r);
+        w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+      }
+      *nonfinite = 1;
+      *at = v;
+    }
+  }
+}
+
+// The guard warps over the cache.
+template <typename T>
+__device__ void guard_cache(const Attend16 &p, const int64_t *loc, uint8_t *ring_base, int *bad, Bars &bars,
+                            Flags *flags) {
+  const int lane = threadIdx.x & 31, g = threadIdx.x - kGuardWarp * 32;
+  volatile int *abort = &flags->abort, *nonfinite = &flags->nonfinite;
+  Ring ring(p.slots);
+  uint32_t n_clear = 0, n_go = 0;
+  bool ok = true;
+  cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
+    const int all = all_see(p, s), none = none_sees(p, s, p.tok), n = s.n[0];
+    bool fresh = k > 0;
+    for (int i = 0; i < n + 2; ++i) {
+      if (i >= 2 && i - 2 < n) {
+        const uint32_t rd = ring.round, sl = ring.step();
+        const int t0 = (s.j0 + i - 2) * kTile;
+        if (t0 + kTile > all && ok) {
+          // The MMA warp has the tile: the phases that the waits below name
+          // are those of this tile and of the segment before.
+          ok = warp_wait(&bars.go, n_go & 1u, p, abort);
+          ++n_go;
+          if (fresh) {
+            // the marks of the segment before are read no more
+            ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
+            fresh = false;
+            if (threadIdx.x < (kGuardWarp + 1) * 32) {
+              if (*nonfinite) {
+                for (int e = lane; e < 3 * kD; e += 32) bad[e] = INT_MAX;
+                __syncwarp();
+                if (lane == 0) *nonfinite = 0;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.cleared);
+            } else {
+              ok = ok && warp_wait(&bars.cleared, n_clear & 1u, p, abort);
+            }
+            ++n_clear;
+          }
+          ok = ok && warp_wait(&bars.full[sl], rd & 1u, p, abort);
+          guard_tile<T>(ring_base + sl * kTileBytes, t0, all, none, g, bad, nonfinite);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&bars.guarded);
+        }
+      }
+      if (i < n) ring.step();
+    }
+    return ok;
+  });
+}
+
+// The segment that starts in this CTA's part and goes on in the CTAs behind,
+// for the combine kernel (one thread).
+__device__ void write_plan(const Attend16 &p, const int64_t *loc) {
+  const int64_t ge = loc[1], total = loc[4];
+  int2 plan = make_int2(-1, 0);
+  Walk16 wk(p, loc);
+  Segment s;
+  while (wk.next(p, s)) {
+    if (s.starts && !s.whole) {
+      const int64_t N = min(static_cast<int64_t>(p.n_cta), total);
+      const int64_t last = ge + (wk.un.nt - wk.j) - 1;  // the segment's last tile
+      plan = make_int2(s.id, static_cast<int>(((last + 1) * N + total - 1) / total - 1));
+    }
+  }
+  p.plan[blockIdx.x] = plan;
+}
+
+// kPaged: the cache's form for more than 64 rows, else prompts.  kLo: bf16
+// weights as two operands (16 bits), so that the result is off by one rounding.
+template <typename T, bool kPaged>
+__global__ void __launch_bounds__(kThreads16, 1)
+    k_attend16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv) {
+  constexpr bool kLo = kPaged && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t *ring_base = smem + 4 * p.q_half, *tail = ring_base + p.slots * kTileBytes;
+  int *bad = reinterpret_cast<int *>(tail + kOffBad);
+  float2 *ml = reinterpret_cast<float2 *>(tail + kOffMl);
+  Bars &bars = *reinterpret_cast<Bars *>(tail + kOffBar);
+  Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
+  volatile int *abort = &flags->abort, *issued = &flags->issued, *nonfinite = &flags->nonfinite;
+  int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
+  const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
+
+  start_cta<512>(bars, flags, bad, row_warps, row_warps);
   pdl_trigger();
   pdl_wait();
-  Segment sg{};
+  Segment prompt{};
+  bool has_prompt = false;
   if constexpr (kPaged) {
     locate16(p, loc, loc + 8);
   } else {
-    // every warp finds the CTA's work by itself
     __syncthreads();
-  }
-  const bool has_prompt = kPaged ? false : find_prompt(p, sg);
-  int64_t my_loc[5];
-  if constexpr (kPaged) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) my_loc[i] = loc[i];
-    __syncthreads();
+    has_prompt = find_prompt(p, prompt);  // every warp by itself
   }
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  // f(segment, number) for each segment of this CTA, until f says stop
+  const uint32_t tmem = flags->tmem;
   auto for_segments = [&](auto &&f) {
-    if constexpr (kPaged) {
-      Walk16 wk(p, my_loc);
-      Segment s;
-      for (uint32_t k = 0; wk.next(p, s); ++k)
-        if (!f(s, k)) return;
-    } else {
-      if (has_prompt) f(sg, 0u);
-    }
-  };
-  // a segment's key tiles hold tokens 128 j ..; below this token every row sees all
-  auto all_see = [&](const Segment &s) { return s.limit(s.row0, p.causal); };
-  auto none_sees = [&](const Segment &s) {
-    const int last = min(s.rows, s.row0 + (kPaged ? 1 : 2) * p.tok) - 1;
-    return s.limit(last, p.causal);
+    if constexpr (kPaged) cache_segments(p, loc, f);
+    else if (has_prompt) f(prompt, 0u);
   };
 
   // registers of the four helper warps go to the softmax threads:
@@ -494,19 +725,15 @@ __global__ void __launch_bounds__(kThreads16, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // ------------------------------------------------------------------ MMA
     const bool leader = lane == 0;
-    uint32_t slot = 0, round = 0;  // next ring slot in the order of use
+    Ring ring(p.slots);
     uint32_t n_p[2] = {0, 0}, n_guard = 0;
     bool ok = true;
     auto take = [&]() {  // waits for the next slot's tile
-      ok = ok && warp_wait(&full[slot], round & 1u, p, abort);
-      const uint32_t s = slot;
-      if (++slot == static_cast<uint32_t>(p.slots)) {
-        slot = 0;
-        ++round;
-      }
-      return s;
+      ok = ok && warp_wait(&bars.full[ring.slot], ring.round & 1u, p, abort);
+      return ring.step();
     };
-    const uint64_t dK = desc128(smem_addr(ring), 1, 64), dV = desc128(smem_addr(ring), kTileBytes / 32, 64);
+    const uint64_t dK = desc128(smem_addr(ring_base), 1, 64),
+                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64);
     const uint32_t q_units = static_cast<uint32_t>(p.q_half) >> 4;
     auto issue_s = [&](int x, int qb, uint32_t sl) {
       tc_fence_after();
@@ -517,18 +744,18 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_ss(tmem + 128 * x, a + (k >> 2) * static_cast<uint64_t>(q_units) + 2 * (k & 3),
-                 b + (k >> 2) * (kTileBytes >> 5) + 2 * (k & 3), idesc16<T>(0), k > 0);
-        umma_commit(&s_full[x]);
+                 b + (k >> 2) * (kTileBytes >> 5) + 2 * (k & 3), idesc16<T>(kTile, 0, 0), k > 0);
+        umma_commit(&bars.s_full[x]);
       }
       __syncwarp();
     };
     auto issue_pv = [&](int x, uint32_t sl, bool first, bool guard) {
-      if (guard && ok && leader) mbar_arrive(guard_go);
+      if (guard && ok && leader) mbar_arrive(&bars.go);
       __syncwarp();
-      ok = ok && warp_wait(&p_full[x], n_p[x] & 1u, p, abort);
+      ok = ok && warp_wait(&bars.p_full[x], n_p[x] & 1u, p, abort);
       ++n_p[x];
       if (guard) {
-        ok = ok && warp_wait(guarded, n_guard & 1u, p, abort);
+        ok = ok && warp_wait(&bars.guarded, n_guard & 1u, p, abort);
         ++n_guard;
       }
       tc_fence_after();
@@ -536,11 +763,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
         const uint64_t b = dV + sl * (kTileBytes >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, b + 128 * k, idesc16<T>(1), !first || k > 0);
+          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, b + 128 * k, idesc16<T>(kTile, 0, 1), !first || k > 0);
         if constexpr (kLo) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * k, b + 128 * k, idesc16<T>(1), 1);
+            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * k, b + 128 * k, idesc16<T>(kTile, 0, 1), 1);
         }
       }
       __syncwarp();
@@ -550,24 +777,23 @@ __global__ void __launch_bounds__(kThreads16, 1)
       __syncwarp();
     };
     for_segments([&](const Segment &s, uint32_t k) {
-      const int all = all_see(s);
+      const int all = all_see(p, s);
       if constexpr (kPaged) {
         const int n = s.n[0], qb = k & 1;
-        ok = ok && warp_wait(&q_full[qb], (k >> 1) & 1u, p, abort);
+        ok = ok && warp_wait(&bars.q_full[qb], (k >> 1) & 1u, p, abort);
         for (int i = 0; i < n + 2 && ok; ++i) {
           const int x = i & 1;
           if (i >= 2 && i - 2 < n) {
-            const int t0 = (s.j0 + i - 2) * kTile;
             const uint32_t sl = take();
-            issue_pv(x, sl, i - 2 < 2, t0 + kTile > all);
-            commit(&freed[sl]);
-            if (i >= n) commit(&o_done[x]);
+            issue_pv(x, sl, i - 2 < 2, (s.j0 + i - 1) * kTile > all);
+            commit(&bars.freed[sl]);
+            if (i >= n) commit(&bars.o_done[x]);
           }
           if (i < n) {
             const uint32_t sl = take();
             issue_s(x, qb, sl);
-            commit(&freed[sl]);
-            if (i == n - 1) commit(&q_free[qb]);
+            commit(&bars.freed[sl]);
+            if (i == n - 1) commit(&bars.q_free[qb]);
           }
         }
       } else {
@@ -576,209 +802,90 @@ __global__ void __launch_bounds__(kThreads16, 1)
         for (int j = 0; j <= n && ok; ++j) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            // the first side to need a tile waits for it, the last frees it
             const int other = s.n[1 - x];
             if (j > 0 && j - 1 < s.n[x]) {
-              // the first side to need a tile waits for it, the last frees it
-              if (x == 0 || j - 1 >= other) v_slot = take();
               const bool first_user = x == 0 || j - 1 >= other;
+              if (first_user) v_slot = take();
               issue_pv(x, v_slot, j == 1, first_user && j * kTile > all);
-              if (x == 1 || j - 1 >= other) commit(&freed[v_slot]);
-              if (j == s.n[x]) commit(&o_done[x]);
+              if (x == 1 || j - 1 >= other) commit(&bars.freed[v_slot]);
+              if (j == s.n[x]) commit(&bars.o_done[x]);
             }
             if (j < s.n[x]) {
-              if (j == 0) ok = ok && warp_wait(&q_full[x], 0, p, abort);
+              if (j == 0) ok = ok && warp_wait(&bars.q_full[x], 0, p, abort);
               if (x == 0 || j >= other) k_slot = take();
               issue_s(x, x, k_slot);
-              if (x == 1 || j >= other) commit(&freed[k_slot]);
+              if (x == 1 || j >= other) commit(&bars.freed[k_slot]);
             }
           }
         }
       }
       return ok;
     });
-    if (*issued) umma_commit_by(leader, mma_done);
+    if (*issued) umma_commit_by(leader, &bars.mma_done);
   } else if (warp == kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // --------------------------------------------------------------- loader
-    uint32_t slot = 0, round = 0;
-    bool ok = true;
-    auto next_slot = [&]() {  // waits until the next slot's last tile was used
-      if (round > 0) ok = ok && warp_wait(&freed[slot], (round + 1) & 1u, p, abort);
-      const uint32_t s = slot;
-      if (++slot == static_cast<uint32_t>(p.slots)) {
-        slot = 0;
-        ++round;
-      }
-      return s;
-    };
-    const uint32_t sq = smem_addr(smem), sr = smem_addr(ring);
-    // box of a Q tile: 64 dims x GB heads x tok tokens
-    auto load_q = [&](int qb, const Segment &s, int row) {
-      if (lane == 0 && ok) {
-        mbar_arrive_expect_tx(&q_full[qb], static_cast<uint32_t>(p.tok * p.GB * kD * 2));
+    if constexpr (kPaged) {
+      load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), 2, bars, abort);
+    } else if (has_prompt) {
+      const Segment &s = prompt;
+      const uint32_t sq = smem_addr(smem), sr = smem_addr(ring_base);
+      Ring ring(p.slots);
+      bool ok = true;
+      // box of a Q tile: 64 dims x G heads x tok tokens
+      auto load_q = [&](int x) {
+        if (s.n[x] && lane == 0) {
+          mbar_arrive_expect_tx(&bars.q_full[x], static_cast<uint32_t>(p.R * kD * 2));
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          tma_3d(sq + (2 * qb + hf) * p.q_half, &mq, 64 * hf, s.h * p.G + s.chunk * kTile, row, &q_full[qb]);
-      }
-      __syncwarp();
-    };
-    for_segments([&](const Segment &s, uint32_t k) {
-      if constexpr (kPaged) {
-        const int qb = k & 1;
-        if (k >= 2) ok = ok && warp_wait(&q_free[qb], ((k >> 1) + 1) & 1u, p, abort);
-        load_q(qb, s, s.b * p.nq + s.row0);
-        const int end = none_sees(s);
-        const int box = min(kTile, 1 << p.ps_shift), boxes = kTile / box;
-        // lane 2 i + hf loads half hf of the tile's i-th page
-        const int hf = lane & 1, part = lane >> 1;
-        auto page_of = [&](int i) {  // row of this lane's part of tile i: -1 if nothing of it is seen
-          const int t = (s.j0 + i) * kTile + part * box;
-          if (i >= s.n[0] || part >= boxes || t >= end) return -1;
-          const int page = p.page_table[static_cast<int64_t>(s.b) * p.max_pages + (t >> p.ps_shift)];
-          return page < 0 || page >= p.num_pages ? -2 : page;
-        };
-        int pages[3] = {-1, -1, -1};  // of tiles i, i - 1, i - 2
-        int ahead = page_of(0);
-        for (int i = 0; i < s.n[0] + 2 && ok; ++i) {
-          pages[2] = pages[1];
-          pages[1] = pages[0];
-          pages[0] = ahead;
-          ahead = page_of(i + 1);
-          if (pages[0] == -2) {
-            set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
-            pages[0] = 0;
-          }
-          auto load = [&](int page, int tile, int kv) {
-            const uint32_t sl = next_slot();
-            if (!ok) return;
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128u;
-            if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
-            __syncwarp();
-            if (page >= 0) {
-              const int off = ((s.j0 + tile) * kTile + part * box) & ((1 << p.ps_shift) - 1);
-              // one row per token: below 2^31 rows, checked on the host
-              const int row = ((page * 2 + kv) * p.H + s.h) * (1 << p.ps_shift) + off;
-              tma_2d(sr + sl * kTileBytes + hf * (kTileBytes / 2) + part * box * 128, &mk, 64 * hf, row, &full[sl]);
-            }
-            __syncwarp();
-          };
-          if (i >= 2 && i - 2 < s.n[0]) load(pages[2], i - 2, 1);
-          if (i < s.n[0]) load(pages[0], i, 0);
+          for (int hf = 0; hf < 2; ++hf)
+            tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + x * p.tok, &bars.q_full[x]);
         }
-      } else {
-        if (s.n[0]) load_q(0, s, s.kv0 + s.row0);
-        const int n = max(s.n[0], s.n[1]);
-        for (int j = 0; j < n && ok; ++j) {
+        __syncwarp();
+      };
+      load_q(0);
+      const int n = max(s.n[0], s.n[1]);
+      for (int j = 0; j < n && ok; ++j) {
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t sl = next_slot();
-            if (lane == 0 && ok) {
-              mbar_arrive_expect_tx(&full[sl], kTileBytes);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (ring.round > 0) ok = ok && warp_wait(&bars.freed[ring.slot], (ring.round - 1) & 1u, p, abort);
+          if (!ok) break;
+          const uint32_t sl = ring.step();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars.full[sl], kTileBytes);
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile,
-                       &full[sl]);
-            }
-            __syncwarp();
-            if (j == 0 && kv == 0 && s.n[1]) load_q(1, s, s.kv0 + s.row0 + p.tok);
+            for (int hf = 0; hf < 2; ++hf)
+              tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile,
+                     &bars.full[sl]);
           }
+          __syncwarp();
+          if (j == 0 && kv == 0) load_q(1);
         }
       }
-      return ok;
-    });
-    if (!ok) {
-      // copies may be in flight: wait for those of every slot's last use
-      for (uint32_t i = 0; i < static_cast<uint32_t>(p.slots); ++i) {
-        const uint32_t used = round + (i < slot ? 1u : 0u);
-        if (used > 0) mbar_wait(&full[i], (used - 1) & 1u, p.status, nullptr);
-      }
+      drain(p, ring, bars, ok);
     }
   } else if (warp >= kGuardWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // --------------------------------------------------------------- guards
-    uint32_t slot = 0, round = 0, n_clear = 0, n_go = 0;
-    bool ok = true;
-    const int g = tid - kGuardWarp * 32;
-    for_segments([&](const Segment &s, uint32_t k) {
-      const int all = all_see(s), none_after = none_sees(s);
-      const int n = kPaged ? s.n[0] : max(s.n[0], s.n[1]);
-      bool fresh = k > 0;
-      // the order of use: K0 K1 V0 K2 V1 .. (cache), K0 V0 K1 V1 .. (prompts)
-      auto visit = [&](int tile, bool is_v) {
-        const uint32_t sl = slot, rd = round;
-        if (++slot == static_cast<uint32_t>(p.slots)) {
-          slot = 0;
-          ++round;
-        }
-        const int t0 = (s.j0 + tile) * kTile;
-        if (!is_v || t0 + kTile <= all || !ok) return;
-        // The MMA warp has the tile: the phases that the waits below name are
-        // those of this tile and of the segment before.
-        ok = warp_wait(guard_go, n_go & 1u, p, abort);
+    if constexpr (kPaged) {
+      guard_cache<T>(p, loc, ring_base, bad, bars, flags);
+    } else if (has_prompt) {
+      const Segment &s = prompt;
+      const int all = all_see(p, s), none = none_sees(p, s, 2 * p.tok), n = max(s.n[0], s.n[1]);
+      Ring ring(p.slots);
+      uint32_t n_go = 0;
+      bool ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        ring.step();
+        const uint32_t rd = ring.round, sl = ring.step();
+        if ((j + 1) * kTile <= all) continue;
+        ok = warp_wait(&bars.go, n_go & 1u, p, abort) && warp_wait(&bars.full[sl], rd & 1u, p, abort);
         ++n_go;
-        if (fresh) {
-          // the marks of the segment before are read no more
-          ok = ok && warp_wait(seg_done, (k - 1) & 1u, p, abort);
-          fresh = false;
-          if (warp == kGuardWarp) {
-            if (*nonfinite) {
-              for (int i = lane; i < 3 * kD; i += 32) bad[i] = INT_MAX;
-              __syncwarp();
-              if (lane == 0) *nonfinite = 0;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cleared);
-          } else {
-            ok = ok && warp_wait(cleared, n_clear & 1u, p, abort);
-          }
-          ++n_clear;
-        }
-        ok = ok && warp_wait(&full[sl], rd & 1u, p, abort);
-        uint8_t *tile_v = ring + sl * kTileBytes;
-        const uint32_t mask = exponent_mask<T>();
-        for (int r = max(0, all - t0) + (g >> 4); r < kTile; r += 4) {
-          const int chunk = g & 15;  // 16-byte chunk: half chunk / 8, swizzled by the row
-          uint4 *at = reinterpret_cast<uint4 *>(tile_v + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (chunk & 7) * 16);
-          if (t0 + r >= none_after) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-          }
-          uint4 v = *at;
-          uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
-          if (any) {
-            const int dim0 = (chunk >> 3) * 64 + (((chunk & 7) ^ (r & 7)) * 8);
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu, m = mask & 0xffffu;
-              if ((x & m) != m) continue;
-              const int kind = (x & 0x7fffu) != m ? 2 : (x >> 15);
-              atomicMin(&bad[kind * kD + dim0 + e], t0 + r);
-              w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-            }
-            *nonfinite = 1;
-            *at = v;
-          }
-        }
+        if (!ok) break;
+        guard_tile<T>(ring_base + sl * kTileBytes, j * kTile, all, none, tid - kGuardWarp * 32, bad, nonfinite);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(guarded);
-      };
-      if constexpr (kPaged) {
-        for (int i = 0; i < n + 2; ++i) {
-          if (i >= 2 && i - 2 < n) visit(i - 2, true);
-          if (i < n) visit(i, false);
-        }
-      } else {
-        for (int j = 0; j < n; ++j) {
-          visit(j, false);
-          visit(j, true);
-        }
+        if (lane == 0) mbar_arrive(&bars.guarded);
       }
-      return ok;
-    });
+    }
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -789,16 +896,12 @@ __global__ void __launch_bounds__(kThreads16, 1)
     uint32_t n_s = 0, n_o1 = 0;
     bool ok = true;
     // one row's sum of products, times f, plus what the guards took out
-    auto finish = [&](const Segment &s, int lim, float (&o)[32], int col, float f) {
+    auto finish = [&](int lim, float (&o)[32], int col, float f) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= f;
       if (*nonfinite) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (bad[col + i] < lim) o[i] += INFINITY;
-          if (bad[kD + col + i] < lim) o[i] -= INFINITY;
-          if (bad[2 * kD + col + i] < lim) o[i] = NAN;
-        }
+        for (int i = 0; i < 32; ++i) o[i] = with_nonfinite(o[i], bad, col + i, lim);
       }
     };
     auto store16 = [&](T *dst, const float (&o)[32]) {
@@ -817,24 +920,24 @@ __global__ void __launch_bounds__(kThreads16, 1)
       float ref = -INFINITY, l = 0.f;
       for (int i = 0; i < n && ok; ++i) {
         const int t0 = (s.j0 + (kPaged ? 2 * i + x : i)) * kTile;
-        ok = warp_wait(&s_full[x], n_s & 1u, p, abort);
+        ok = warp_wait(&bars.s_full[x], n_s & 1u, p, abort);
         ++n_s;
         // Side 1's O and sums are merged by side 0 before it writes them again.
         // (Its scores are here, so side 0 is past segment k - 2 and the parity
         // is that of k - 1.)
-        if (kPaged && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(seg_done, (k - 1) & 1u, p, abort);
+        if (kPaged && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
         if (!ok) break;
         tc_fence_after();
         softmax_tile<T, kLo>(ts, to, p.c, lim - t0, i == 0, ref, l);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&bars.p_full[x]);
       }
       if (!ok) return false;
       const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
       if constexpr (!kPaged) {
         if (n == 0) return true;
-        ok = warp_wait(&o_done[x], 0, p, abort);
+        ok = warp_wait(&bars.o_done[x], 0, p, abort);
         if (!ok) return false;
         tc_fence_after();
         const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -844,20 +947,21 @@ __global__ void __launch_bounds__(kThreads16, 1)
         for (int col = 0; col < kD; col += 32) {
           float o[32];
           tmem_ld32(to + col, o);
-          finish(s, lim, o, col, inv);
+          finish(lim, o, col, inv);
           if (valid) store16(dst + col, o);
         }
       } else if (x == 1) {
         if (n > 0) {
           ml[r] = make_float2(sub, l);
           __syncwarp();
-          if (lane == 0) mbar_arrive(side1);
+          if (lane == 0) mbar_arrive(&bars.side1);
         }
       } else {
         const bool both = s.n[0] > 1;
-        ok = warp_wait(&o_done[0], k & 1u, p, abort);
+        ok = warp_wait(&bars.o_done[0], k & 1u, p, abort);
         if (both) {
-          ok = ok && warp_wait(&o_done[1], n_o1 & 1u, p, abort) && warp_wait(side1, n_o1 & 1u, p, abort);
+          ok = ok && warp_wait(&bars.o_done[1], n_o1 & 1u, p, abort) &&
+               warp_wait(&bars.side1, n_o1 & 1u, p, abort);
           ++n_o1;
         }
         if (!ok) return false;
@@ -874,8 +978,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
         // whole: the result; else a record for the combine kernel
-        float *rec = p.records + (static_cast<int64_t>(2) * blockIdx.x + (s.starts ? 1 : 0)) *
-                                     (static_cast<int64_t>(p.row_stride) * (kD + 2));
+        float *rec = record(p, 2 * blockIdx.x + (s.starts ? 1 : 0));
         T *dst = static_cast<T *>(p.out) + ((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq +
                                             static_cast<int64_t>(s.h) * p.G + hq) * kD;
         if (valid && !s.whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
@@ -889,7 +992,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
           }
-          finish(s, lim, o, col, s.whole ? inv : 1.f);
+          finish(lim, o, col, s.whole ? inv : 1.f);
           if (valid) {
             if (s.whole) {
               store16(dst + col, o);
@@ -903,38 +1006,366 @@ __global__ void __launch_bounds__(kThreads16, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(seg_done);
+        if (lane == 0) mbar_arrive(&bars.seg_done);
       }
       return true;
     });
   }
   if constexpr (kPaged) {
-    // the segment that starts here and goes on in the CTAs behind, for the combine kernel
-    if (tid == 0) {
-      const int64_t gs = my_loc[0], ge = my_loc[1], total = my_loc[4];
-      int2 plan = make_int2(-1, 0);
-      if (gs < ge) {
-        Walk16 wk(p, my_loc);
-        Segment s;
-        while (wk.next(p, s)) {
-          if (s.starts && !s.whole) {
-            const int64_t N = min(static_cast<int64_t>(p.n_cta), total);
-            const int64_t last = ge + (wk.un.nt - wk.j) - 1;  // the segment's last tile
-            plan = make_int2(s.id, static_cast<int>(((last + 1) * N + total - 1) / total - 1));
+    if (tid == 0) write_plan(p, loc);
+  }
+  end_cta<512>(bars, flags, p);
+}
+
+// ------------------------------------------------- cache, up to 64 query rows
+// The same walk with tokens as the products' M: a step of a few query rows is
+// bound by the bytes of the cache, and the form above would spend a softmax of
+// 128 rows and two 128-row products on each key tile.  Here
+//   S^T[128 tokens x NR rows] = K Q^T,  O^T[128 dims x 2 NR] += V^T [P | P'],
+// with P the weights' 16-bit parts and, for bf16, P' their remainders in NR
+// more columns, added at the end.  K and V are the A operands from shared
+// memory (V read dims-major), Q and P the narrow B operands.  A softmax thread
+// owns a token; the sides share each tile and take half of its rows each.  No
+// row spans a thread, so the rows' references are common to a side's 128
+// threads (shared memory) and change only when some score passes one by 2^8
+// (one barrier with a vote per tile); the sums stay with the threads until the
+// segment ends.  S^T has two buffers: tile i + 1's scores are computed while
+// tile i's weights are.  P goes to shared memory as 16-byte pieces,
+// [8-row group][token].
+template <typename T, int NR>
+struct Cols {
+  static constexpr bool kLo = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kSide = NR / 2;                 // rows of a side
+  static constexpr int kN = kLo ? 2 * NR : NR;         // columns of O^T
+  static constexpr int kQBufs = NR == 64 ? 1 : 2;
+  static constexpr int kPBufs = NR == 64 ? 1 : 2;
+  static constexpr int kSlots = NR == 16 ? 6 : 5;
+  static constexpr int kQBytes = NR * kD * 2;
+  static constexpr int kPBytes = kN * kTile * 2;
+  static constexpr int kP = kQBufs * kQBytes;
+  static constexpr int kRing = kP + kPBufs * kPBytes;
+  static constexpr int kTail = kRing + kSlots * kTileBytes;
+  // references, what an O column is multiplied by, four warps' maxima or sums of each row
+  static constexpr int kRefs = kTail + kTailBytes;
+  static constexpr int kFactor = kRefs + NR * 4;
+  static constexpr int kPart = kFactor + NR * 4;
+  static constexpr int kBytes = kPart + 4 * NR * 4;
+  static constexpr uint32_t kColO = 2 * NR;            // S^T buffers at 0 and NR
+  static constexpr uint32_t kCols = kColO + kN <= 64 ? 64 : kColO + kN <= 128 ? 128 : 256;
+  static_assert(kRing % 1024 == 0 && kBytes <= 227 * 1024 && kColO + kN <= kCols, "layout");
+};
+
+// barrier of a side's 128 threads with a vote
+__device__ __forceinline__ bool side_any(int x, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred a, b;\n setp.ne.u32 a, %2, 0;\n barrier.cta.red.or.pred b, %1, 128, a;\n selp.u32 %0, 1, 0, "
+      "b;\n}\n"
+      : "=r"(any)
+      : "r"(x + 1), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void side_sync(int x) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(x + 1) : "memory");
+}
+// maximum over a warp that keeps a NaN
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float y;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
+}
+
+// N columns of this thread's tensor-memory lane
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&v)[N]) {
+  if constexpr (N == 8) tmem_ld8(addr, v);
+  else if constexpr (N == 16) tmem_ld16(addr, v);
+  else tmem_ld32(addr, v);
+}
+
+template <typename T, int NR>
+__global__ void __launch_bounds__(kThreads16, 1)
+    k_cols16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+  using C = Cols<T, NR>;
+  constexpr bool kLo = C::kLo;
+  constexpr int SR = C::kSide;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t *ring_base = smem + C::kRing, *tail = smem + C::kTail;
+  int *bad = reinterpret_cast<int *>(tail + kOffBad);
+  Bars &bars = *reinterpret_cast<Bars *>(tail + kOffBar);
+  Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
+  volatile int *abort = &flags->abort, *issued = &flags->issued, *nonfinite = &flags->nonfinite;
+  int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
+  const int soft_warps = p.R > SR ? 8 : 4;  // a side without rows rests
+
+  start_cta<C::kCols>(bars, flags, bad, soft_warps, soft_warps);
+  // Q rows that no copy writes are zero
+  for (int i = tid; i < C::kP / 16; i += kThreads16) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
+  locate16(p, loc, loc + 8);
+  tc_fence_after();
+  const uint32_t tmem = flags->tmem;
+
+  // (64 rows: as k_attend16, registers go to the softmax threads)
+  if (warp == kMmaWarp) {
+    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ------------------------------------------------------------------ MMA
+    const bool leader = lane == 0;
+    Ring ring(C::kSlots);
+    uint32_t n_p = 0, n_s = 0, n_guard = 0;  // tiles, guarded tiles so far
+    bool ok = true;
+    auto take = [&]() {
+      ok = ok && warp_wait(&bars.full[ring.slot], ring.round & 1u, p, abort);
+      return ring.step();
+    };
+    auto commit = [&](uint64_t *bar) {
+      if (leader && ok) umma_commit(bar);
+      __syncwarp();
+    };
+    const uint64_t dK = desc128(smem_addr(ring_base), 1, 64),
+                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64);
+    cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
+      const int all = all_see(p, s), n = s.n[0];
+      const uint32_t qb = k % C::kQBufs, use = k / C::kQBufs;
+      ok = ok && warp_wait(&bars.q_full[qb], use & 1u, p, abort);
+      for (int i = 0; i < n + 2 && ok; ++i) {
+        // The ring holds K0 K1 V0 K2 V1 ..: the scores of tile i go first, to
+        // the buffer that tile i - 2 left (its weights were waited for below).
+        const bool has_v = i >= 2 && i - 2 < n;
+        uint32_t v_slot = 0;
+        if (has_v) v_slot = take();
+        if (has_v) {
+          const bool guard = (s.j0 + i - 1) * kTile > all;
+          if (guard && leader && ok) mbar_arrive(&bars.go);
+          __syncwarp();
+          ok = ok && warp_wait(&bars.p_full[n_p & 1u], (n_p >> 1) & 1u, p, abort);
+          if (guard) {
+            ok = ok && warp_wait(&bars.guarded, n_guard & 1u, p, abort);
+            ++n_guard;
+          }
+          tc_fence_after();
+          if (leader && ok) {
+            const uint64_t a = dV + v_slot * (kTileBytes >> 4);
+            const uint64_t b = desc_plain(smem_addr(smem + C::kP + n_p % C::kPBufs * C::kPBytes), 8, 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mma_ss(tmem + C::kColO, a + 128 * q, b + 16 * q, idesc16<T>(C::kN, 1, 1), i > 2 || q > 0);
+          }
+          __syncwarp();
+          commit(&bars.freed[v_slot]);
+          commit(&bars.o_done[n_p & 1u]);
+          ++n_p;
+        }
+        if (i < n) {
+          const uint32_t sl = take();
+          tc_fence_after();
+          if (leader && ok) {
+            *issued = 1;
+            const uint64_t a = dK + sl * (kTileBytes >> 4);
+            const uint64_t b = desc128(smem_addr(smem) + qb * C::kQBytes, 1, 64);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mma_ss(tmem + (n_s & 1u) * NR, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
+                     b + (q >> 2) * (C::kQBytes >> 5) + 2 * (q & 3), idesc16<T>(NR, 0, 0), q > 0);
+            umma_commit(&bars.s_full[n_s & 1u]);
+          }
+          __syncwarp();
+          ++n_s;
+          commit(&bars.freed[sl]);
+          if (i == n - 1) commit(&bars.q_free[qb]);
+        }
+      }
+      return ok;
+    });
+    if (*issued) umma_commit_by(leader, &bars.mma_done);
+  } else if (warp == kLoadWarp) {
+    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), C::kQBufs, bars, abort);
+  } else if (warp >= kGuardWarp) {
+    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    guard_cache<T>(p, loc, ring_base, bad, bars, flags);
+  } else {
+    // -------------------------------------------------------------- softmax
+    if constexpr (NR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = warp >> 2, t = tid & (kTile - 1), row0 = x * SR;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + row0, to = tmem + lanes + C::kColO + row0;
+    float *refs = reinterpret_cast<float *>(smem + C::kRefs) + row0;
+    float *factor = reinterpret_cast<float *>(smem + C::kFactor) + row0;
+    float *part = reinterpret_cast<float *>(smem + C::kPart) + 4 * row0;
+    const int tok0 = row0 / p.GB, head0 = row0 - tok0 * p.GB;
+    uint32_t n_s = 0;  // tiles so far
+    bool ok = true;
+    // Waits for the product of tile n_s - 1.  The tiles take the two barriers
+    // in turn: that of tile n_s - 3 is done (tile n_s - 1's scores came after
+    // it), so the parity names one phase.
+    auto last_product = [&]() {
+      return warp_wait(&bars.o_done[(n_s - 1) & 1u], ((n_s - 1) >> 1) & 1u, p, abort);
+    };
+    // Every warp of a side goes through the same barriers, after a failed wait too.
+    if (warp < soft_warps) cache_segments(p, loc, [&](const Segment &s, uint32_t) {
+      const int all = all_see(p, s), n = s.n[0];
+      float l[SR];
+#pragma unroll
+      for (int r = 0; r < SR; ++r) l[r] = 0.f;
+      for (int i = 0; i < n; ++i) {
+        const int tok = (s.j0 + i) * kTile + t;
+        ok = ok && warp_wait(&bars.s_full[n_s & 1u], (n_s >> 1) & 1u, p, abort);
+        tc_fence_after();
+        float v[SR];
+        tmem_ld_cols<SR>(ts + (n_s & 1u) * NR, v);
+        if ((s.j0 + i + 1) * kTile > all) {
+          int qi = s.row0 + tok0, head = head0, lim = s.limit(qi, p.causal);
+#pragma unroll
+          for (int r = 0; r < SR; ++r) {
+            if (tok >= lim) v[r] = -INFINITY;
+            if (++head == p.GB) {
+              head = 0;
+              lim = s.limit(++qi, p.causal);
+            }
+          }
+        }
+        // has a score passed its row's reference by kLazy (in log2)?  A NaN has.
+        bool move = i == 0;
+        if (i > 0) {
+#pragma unroll
+          for (int r = 0; r < SR; r += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(refs + r);
+            move |= !(v[r] * p.c <= f.x + kLazy) | !(v[r + 1] * p.c <= f.y + kLazy) |
+                    !(v[r + 2] * p.c <= f.z + kLazy) | !(v[r + 3] * p.c <= f.w + kLazy);
+          }
+        }
+        if (side_any(x, move)) {
+          // the tile's maxima: over a warp's tokens, then over the four warps
+#pragma unroll
+          for (int r = 0; r < SR; ++r) {
+            const float m = warp_max_nan(v[r]);
+            if (lane == 0) part[(warp & 3) * SR + r] = m;
+          }
+          side_sync(x);
+          if (t < SR) {
+            const float m = max3_nan(max3_nan(part[t], part[SR + t], part[2 * SR + t]), part[3 * SR + t],
+                                     part[3 * SR + t]) * p.c;
+            const float old = i == 0 ? -INFINITY : refs[t];
+            const bool up = !(m <= old + kLazy);
+            factor[t] = up ? ex2f(old - m) : 1.f;
+            refs[t] = up ? m : old;
+          }
+          side_sync(x);
+          if (i > 0) {
+            // the last product must be done
+            ok = ok && last_product();
+            tc_fence_after();
+#pragma unroll
+            for (int r = 0; r < SR; ++r) l[r] *= factor[r];
+#pragma unroll
+            for (int c = 0; c < (kLo ? 2 : 1); ++c) {
+              float o[SR];
+              tmem_ld_cols<SR>(to + c * NR, o);
+#pragma unroll
+              for (int r = 0; r < SR; ++r) o[r] *= factor[r];
+              tmem_st_cols<SR>(to + c * NR, o);
+            }
+            tmem_stored();
+          }
+        }
+        // the buffer of P: with one, the last product must have read it; with
+        // two, these scores came behind the product that read it
+        if (C::kPBufs == 1 && n_s > 0) ok = ok && last_product();
+        uint8_t *dst = smem + C::kP + n_s % C::kPBufs * C::kPBytes + (row0 >> 3) * (kTile * 16) + t * 16;
+#pragma unroll
+        for (int g = 0; g < SR; g += 8) {
+          uint32_t w[4], e[4];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(refs + g + j);
+            const float fr[4] = {f.x, f.y, f.z, f.w};
+            float pr[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const float sub = fr[a] == -INFINITY ? 0.f : fr[a] - kShift<T>;
+              pr[a] = ex2f(fmaf(v[g + j + a], p.c, -sub));
+              l[g + j + a] += pr[a];
+            }
+            w[j >> 1] = pack16(pr[0], pr[1], T());
+            w[(j >> 1) + 1] = pack16(pr[2], pr[3], T());
+            if constexpr (kLo) {
+#pragma unroll
+              for (int a = 0; a < 2; ++a)
+                e[(j >> 1) + a] = pack16(pr[2 * a] - __uint_as_float(w[(j >> 1) + a] << 16),
+                                         pr[2 * a + 1] - __uint_as_float(w[(j >> 1) + a] & 0xffff0000u), T());
+            }
+          }
+          *reinterpret_cast<uint4 *>(dst + (g >> 3) * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          if constexpr (kLo)
+            *reinterpret_cast<uint4 *>(dst + ((NR + g) >> 3) * (kTile * 16)) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&bars.p_full[n_s & 1u]);
+        ++n_s;
+      }
+      // the rows' sums over a warp's tokens, then over the four warps
+      side_sync(x);  // the maxima of a last move have been read
+#pragma unroll
+      for (int r = 0; r < SR; ++r) {
+        float a = l[r];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (lane == 0) part[(warp & 3) * SR + r] = a;
+      }
+      side_sync(x);
+      float *rec = record(p, 2 * blockIdx.x + (s.starts ? 1 : 0));
+      if (t < SR) {
+        const float sum = (part[t] + part[SR + t]) + (part[2 * SR + t] + part[3 * SR + t]);
+        factor[t] = !s.whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
+        if (!s.whole && row0 + t < p.R)
+          *reinterpret_cast<float2 *>(rec + 2 * (row0 + t)) =
+              make_float2(refs[t] == -INFINITY ? -INFINITY : refs[t] - kShift<T>, sum);
+      }
+      ok = ok && last_product();
+      tc_fence_after();
+      side_sync(x);
+      // thread t: dim t of the side's rows
+      float o[SR];
+      tmem_ld_cols<SR>(to, o);
+      if constexpr (kLo) {
+        float e[SR];
+        tmem_ld_cols<SR>(to + NR, e);
+#pragma unroll
+        for (int r = 0; r < SR; ++r) o[r] += e[r];
+      }
+      if (ok) {
+        int qi = s.row0 + tok0, head = head0;
+        T *out = static_cast<T *>(p.out) + (static_cast<int64_t>(s.h) * p.G + s.chunk * kTile) * kD + t;
+        const int heads = p.G - s.chunk * kTile;
+#pragma unroll
+        for (int r = 0; r < SR; ++r) {
+          if (row0 + r < p.R && qi < s.rows && head < heads) {
+            float y = o[r] * factor[r];
+            if (*nonfinite) y = with_nonfinite(y, bad, t, s.limit(qi, p.causal));
+            if (s.whole) out[((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq + head) * kD] = to16(y, T());
+            else rec[2 * p.row_stride + (row0 + r) * kD + t] = y;
+          }
+          if (++head == p.GB) {
+            head = 0;
+            ++qi;
           }
         }
       }
-      p.plan[blockIdx.x] = plan;
-    }
+      tc_fence_before();
+      side_sync(x);  // sums and factors are read
+      if (lane == 0 && ok) mbar_arrive(&bars.seg_done);
+      return true;
+    });
   }
-  // the products must complete before tensor memory is released
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
-    if (*issued) mbar_wait(mma_done, 0, p.status, nullptr);
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
-  }
+  if (tid == 0) write_plan(p, loc);
+  end_cta<C::kCols>(bars, flags, p);
 }
 
 // Joins the records of each segment that spans CTAs: block (c, y) the rows 4 y
@@ -952,9 +1383,8 @@ __global__ void __launch_bounds__(128) k_combine16(const Attend16 p) {
   const int b = u / rts, rt = u - b * rts;
   const int qi = rt / p.chunks * p.tok + r / p.GB, hq = rt % p.chunks * kTile + r % p.GB;
   if (r >= p.R || qi >= p.nq || hq >= p.G) return;
-  const int64_t size = static_cast<int64_t>(p.row_stride) * (kD + 2);
   const int first = blockIdx.x, count = plan.y - first + 1;
-  auto rec = [&](int i) { return p.records + (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * size; };
+  auto rec = [&](int i) { return record(p, 2 * (first + i) + (i == 0 ? 1 : 0)); };
   float m = -INFINITY;
   for (int i = lane; i < count; i += 32) m = fmaxf(m, rec(i)[2 * r]);
 #pragma unroll
@@ -1032,14 +1462,29 @@ void row_tiles(Attend16 &p, int group) {
   p.tok = kTile / p.GB;
 }
 
-template <typename T, bool kPaged>
-cudaError_t launch16(const Attend16 &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                     unsigned grid, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(4) * p.q_half + static_cast<size_t>(p.slots) * kTileBytes + kTailBytes;
-  const cudaError_t e = cudaFuncSetAttribute(k_attend16<T, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_attend16<T, kPaged>, dim3(grid), dim3(kThreads16), smem, stream, p, mq, mk, mv);
+// a kernel's launch with its dynamic shared memory
+template <typename... P, typename... A>
+cudaError_t launch_tiles(void (*kernel)(P...), int smem, unsigned grid, cudaStream_t stream, const A &...args) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(kThreads16), smem, stream, args...);
+}
+int rows_smem(const Attend16 &p) { return 4 * p.q_half + p.slots * kTileBytes + kOffMl + kTile * 8; }
+
+template <typename T, int NR>
+cudaError_t launch_cols(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid, cudaStream_t stream) {
+  p.slots = Cols<T, NR>::kSlots;
+  p.q_half = Cols<T, NR>::kQBytes / 2;
+  return launch_tiles(k_cols16<T, NR>, Cols<T, NR>::kBytes, grid, stream, p, mq, mk);
+}
+template <typename T>
+cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid,
+                         cudaStream_t stream) {
+  if (p.R <= 16) return launch_cols<T, 16>(p, mq, mk, grid, stream);
+  if (p.R <= 32) return launch_cols<T, 32>(p, mq, mk, grid, stream);
+  if (p.R <= 64) return launch_cols<T, 64>(p, mq, mk, grid, stream);
+  p.slots = 5;
+  p.q_half = kTileBytes / 2;
+  return launch_tiles(k_attend16<T, true>, rows_smem(p), grid, stream, p, mq, mk, mk);
 }
 
 // the cache's row tiles: rows, and the stride of a record's rows
@@ -1080,9 +1525,10 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   // pairs of row tiles: no more than one per 2 tok tokens and one per sequence
   const int64_t grid = (static_cast<int64_t>(n_tok) / (2 * p.tok) + batch) * p.H;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const unsigned g = static_cast<unsigned>(grid);
   return dtype == ISOQUANT_BF16
-             ? launch16<__nv_bfloat16, false>(p, mq, mk, mv, static_cast<unsigned>(grid), stream)
-             : launch16<__half, false>(p, mq, mk, mv, static_cast<unsigned>(grid), stream);
+             ? launch_tiles(k_attend16<__nv_bfloat16, false>, rows_smem(p), g, stream, p, mq, mk, mv)
+             : launch_tiles(k_attend16<__half, false>, rows_smem(p), g, stream, p, mq, mk, mv);
 }
 
 size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s) {
@@ -1111,9 +1557,6 @@ cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_ca
   p.n_cta = ctx->num_sms;
   p.plan = static_cast<int2 *>(ws);
   p.records = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(p.n_cta));
-  // up to 64 rows a Q buffer's halves need 64 rows each, which leaves room for another slot
-  p.slots = p.R <= kTile / 2 ? 6 : 5;
-  p.q_half = p.R <= kTile / 2 ? kTileBytes / 4 : kTileBytes / 2;
   p.out = out;
   p.status = ctx->status;
   CUtensorMap mq, mk;
@@ -1127,8 +1570,8 @@ cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_ca
     return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(p.n_cta);
   const bool bf = cache->dtype == ISOQUANT_BF16;
-  const cudaError_t e = bf ? launch16<__nv_bfloat16, true>(p, mq, mk, mk, grid, stream)
-                           : launch16<__half, true>(p, mq, mk, mk, grid, stream);
+  const cudaError_t e = bf ? launch_cache<__nv_bfloat16>(p, mq, mk, grid, stream)
+                           : launch_cache<__half>(p, mq, mk, grid, stream);
   if (e != cudaSuccess) return e;
   const dim3 cg(grid, static_cast<unsigned>((p.R + 3) / 4)), block(128);
   return bf ? launch_pdl(k_combine16<__nv_bfloat16>, cg, block, 0, stream, p)
