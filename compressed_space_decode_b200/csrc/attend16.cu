@@ -45,9 +45,9 @@ namespace {
 
 constexpr int kTile = 128;                  // rows of a row tile, tokens of a key tile
 constexpr int kTileBytes = kTile * kD * 2;  // 32 KB
-constexpr int kThreads16 = 3 * 128;         // two sides, then the MMA, loader and two guard warps
 constexpr int kMaxSlots = 6;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kGuardWarp = 2;  // and 3; then the sides' softmax warps
+constexpr int kThreads16 = 3 * 128;         // k_attend16: two sides
 // shared memory behind the tiles
 constexpr int kOffBad = 0;                      // first token with +inf, -inf, NaN of each dim
 constexpr int kOffBar = kOffBad + 3 * kD * 4;   // barriers
@@ -254,11 +254,12 @@ struct Unit {
 
 // The CTA's part [gs, ge) of all tiles, and the (unit, tile offset) where it
 // starts.  loc: {gs, ge, unit, offset, total}; ends with __syncthreads.
+template <int NT>
 __device__ void locate16(const Attend16 &p, int64_t *loc, int64_t *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int U = p.B * ((p.nq + p.tok - 1) / p.tok * p.chunks);
-  const int u0 = static_cast<int>(static_cast<int64_t>(U) * tid / kThreads16),
-            u1 = static_cast<int>(static_cast<int64_t>(U) * (tid + 1) / kThreads16);
+  const int u0 = static_cast<int>(static_cast<int64_t>(U) * tid / NT),
+            u1 = static_cast<int>(static_cast<int64_t>(U) * (tid + 1) / NT);
   int64_t mine = 0;
   Unit un;
   for (int u = u0; u < u1; ++u) {
@@ -275,7 +276,7 @@ __device__ void locate16(const Attend16 &p, int64_t *loc, int64_t *scratch) {
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
-  for (int w = 0; w < kThreads16 / 32; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
@@ -481,7 +482,7 @@ __device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, in
     bars.init(p_count, seg_count);
     flags->abort = flags->issued = flags->nonfinite = 0;
   }
-  for (int i = threadIdx.x; i < 3 * kD; i += kThreads16) bad[i] = INT_MAX;
+  for (int i = threadIdx.x; i < 3 * kD; i += blockDim.x) bad[i] = INT_MAX;
 }
 // the products must complete before tensor memory is released
 template <uint32_t COLS>
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
   Segment prompt{};
   bool has_prompt = false;
   if constexpr (kPaged) {
-    locate16(p, loc, loc + 8);
+    locate16<kThreads16>(p, loc, loc + 8);
   } else {
     __syncthreads();
     has_prompt = find_prompt(p, prompt);  // every warp by itself
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
       }
       drain(p, ring, bars, ok);
     }
-  } else if (warp >= kGuardWarp) {
+  } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if constexpr (kPaged) {
       guard_cache<T>(p, loc, ring_base, bad, bars, flags);
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int x = warp >> 2, r = tid & (kTile - 1);
+    const int x = (warp >> 2) - 1, r = tid & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
     const int r_tok = r / p.GB, r_head = r - r_tok * p.GB;
@@ -1025,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
 // with P the weights' 16-bit parts and, for bf16, P' their remainders in NR
 // more columns, added at the end.  K and V are the A operands from shared
 // memory (V read dims-major), Q and P the narrow B operands.  A softmax thread
-// owns a token; the sides share each tile and take half of its rows each.  No
+// owns a token; two (four) sides share each tile and take 8 or 16 rows each.  No
 // row spans a thread, so the rows' references are common to a side's 128
 // threads (shared memory) and change only when some score passes one by 2^8
 // (one barrier with a vote per tile); the sums stay with the threads until the
@@ -1035,7 +1036,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
 template <typename T, int NR>
 struct Cols {
   static constexpr bool kLo = std::is_same<T, __nv_bfloat16>::value;
-  static constexpr int kSide = NR / 2;                 // rows of a side
+  static constexpr int kSide = NR == 16 ? 8 : 16;      // rows of a side
+  static constexpr int kThreads = (4 + NR / kSide * 4) * 32;
   static constexpr int kN = kLo ? 2 * NR : NR;         // columns of O^T
   static constexpr int kQBufs = NR == 64 ? 1 : 2;
   static constexpr int kPBufs = NR == 64 ? 1 : 2;
@@ -1045,9 +1047,13 @@ struct Cols {
   static constexpr int kP = kQBufs * kQBytes;
   static constexpr int kRing = kP + kPBufs * kPBytes;
   static constexpr int kTail = kRing + kSlots * kTileBytes;
-  // references, what an O column is multiplied by, four warps' maxima or sums of each row
+  // Each row's reference, the score above which it moves, what is added to a
+  // score's logarithm, what an O column is multiplied by, and four warps'
+  // maxima or sums.
   static constexpr int kRefs = kTail + kTailBytes;
-  static constexpr int kFactor = kRefs + NR * 4;
+  static constexpr int kLimits = kRefs + NR * 4;
+  static constexpr int kSubs = kLimits + NR * 4;
+  static constexpr int kFactor = kSubs + NR * 4;
   static constexpr int kPart = kFactor + NR * 4;
   static constexpr int kBytes = kPart + 4 * NR * 4;
   static constexpr uint32_t kColO = 2 * NR;            // S^T buffers at 0 and NR
@@ -1085,7 +1091,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&v)[N]) {
 }
 
 template <typename T, int NR>
-__global__ void __launch_bounds__(kThreads16, 1)
+__global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
     k_cols16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
   using C = Cols<T, NR>;
   constexpr bool kLo = C::kLo;
@@ -1098,21 +1104,19 @@ __global__ void __launch_bounds__(kThreads16, 1)
   Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
   volatile int *abort = &flags->abort, *issued = &flags->issued, *nonfinite = &flags->nonfinite;
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
-  const int soft_warps = p.R > SR ? 8 : 4;  // a side without rows rests
+  const int soft_warps = (p.R + SR - 1) / SR * 4;  // sides without rows rest
 
   start_cta<C::kCols>(bars, flags, bad, soft_warps, soft_warps);
   // Q rows that no copy writes are zero
-  for (int i = tid; i < C::kP / 16; i += kThreads16) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < C::kP / 16; i += C::kThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   pdl_trigger();
   pdl_wait();
-  locate16(p, loc, loc + 8);
+  locate16<C::kThreads>(p, loc, loc + 8);
   tc_fence_after();
   const uint32_t tmem = flags->tmem;
 
-  // (64 rows: as k_attend16, registers go to the softmax threads)
   if (warp == kMmaWarp) {
-    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // ------------------------------------------------------------------ MMA
     const bool leader = lane == 0;
     Ring ring(C::kSlots);
@@ -1183,18 +1187,17 @@ __global__ void __launch_bounds__(kThreads16, 1)
     });
     if (*issued) umma_commit_by(leader, &bars.mma_done);
   } else if (warp == kLoadWarp) {
-    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), C::kQBufs, bars, abort);
-  } else if (warp >= kGuardWarp) {
-    if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  } else if (warp < 4) {
     guard_cache<T>(p, loc, ring_base, bad, bars, flags);
   } else {
     // -------------------------------------------------------------- softmax
-    if constexpr (NR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int x = warp >> 2, t = tid & (kTile - 1), row0 = x * SR;
+    const int x = (warp >> 2) - 1, t = tid & (kTile - 1), row0 = x * SR;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + row0, to = tmem + lanes + C::kColO + row0;
     float *refs = reinterpret_cast<float *>(smem + C::kRefs) + row0;
+    float *limits = reinterpret_cast<float *>(smem + C::kLimits) + row0;
+    float *subs = reinterpret_cast<float *>(smem + C::kSubs) + row0;
     float *factor = reinterpret_cast<float *>(smem + C::kFactor) + row0;
     float *part = reinterpret_cast<float *>(smem + C::kPart) + 4 * row0;
     const int tok0 = row0 / p.GB, head0 = row0 - tok0 * p.GB;
@@ -1207,11 +1210,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
       return warp_wait(&bars.o_done[(n_s - 1) & 1u], ((n_s - 1) >> 1) & 1u, p, abort);
     };
     // Every warp of a side goes through the same barriers, after a failed wait too.
-    if (warp < soft_warps) cache_segments(p, loc, [&](const Segment &s, uint32_t) {
+    if (warp < 4 + soft_warps) cache_segments(p, loc, [&](const Segment &s, uint32_t) {
       const int all = all_see(p, s), n = s.n[0];
-      float l[SR];
+      float2 l[SR / 2];
 #pragma unroll
-      for (int r = 0; r < SR; ++r) l[r] = 0.f;
+      for (int r = 0; r < SR / 2; ++r) l[r] = make_float2(0.f, 0.f);
       for (int i = 0; i < n; ++i) {
         const int tok = (s.j0 + i) * kTile + t;
         ok = ok && warp_wait(&bars.s_full[n_s & 1u], (n_s >> 1) & 1u, p, abort);
@@ -1229,17 +1232,16 @@ __global__ void __launch_bounds__(kThreads16, 1)
             }
           }
         }
-        // has a score passed its row's reference by kLazy (in log2)?  A NaN has.
-        bool move = i == 0;
+        // has a score passed its row's limit?  A NaN has.
+        bool stay = i > 0;
         if (i > 0) {
 #pragma unroll
           for (int r = 0; r < SR; r += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(refs + r);
-            move |= !(v[r] * p.c <= f.x + kLazy) | !(v[r + 1] * p.c <= f.y + kLazy) |
-                    !(v[r + 2] * p.c <= f.z + kLazy) | !(v[r + 3] * p.c <= f.w + kLazy);
+            const float4 f = *reinterpret_cast<const float4 *>(limits + r);
+            stay = stay && v[r] <= f.x && v[r + 1] <= f.y && v[r + 2] <= f.z && v[r + 3] <= f.w;
           }
         }
-        if (side_any(x, move)) {
+        if (side_any(x, !stay)) {
           // the tile's maxima: over a warp's tokens, then over the four warps
 #pragma unroll
           for (int r = 0; r < SR; ++r) {
@@ -1252,8 +1254,12 @@ __global__ void __launch_bounds__(kThreads16, 1)
                                      part[3 * SR + t]) * p.c;
             const float old = i == 0 ? -INFINITY : refs[t];
             const bool up = !(m <= old + kLazy);
+            const float ref = up ? m : old;
             factor[t] = up ? ex2f(old - m) : 1.f;
-            refs[t] = up ? m : old;
+            refs[t] = ref;
+            // (a reference of +inf keeps its limit at +inf: only a NaN is above)
+            limits[t] = ref == INFINITY ? INFINITY : (ref + kLazy) / p.c;
+            subs[t] = ref == -INFINITY ? 0.f : kShift<T> - ref;
           }
           side_sync(x);
           if (i > 0) {
@@ -1261,7 +1267,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
             ok = ok && last_product();
             tc_fence_after();
 #pragma unroll
-            for (int r = 0; r < SR; ++r) l[r] *= factor[r];
+            for (int r = 0; r < SR; r += 2)
+              l[r >> 1] = __fmul2_rn(l[r >> 1], *reinterpret_cast<const float2 *>(factor + r));
 #pragma unroll
             for (int c = 0; c < (kLo ? 2 : 1); ++c) {
               float o[SR];
@@ -1273,36 +1280,32 @@ __global__ void __launch_bounds__(kThreads16, 1)
             tmem_stored();
           }
         }
+        uint32_t w[SR / 2], e[SR / 2];  // weights and their remainders, two rows each
+#pragma unroll
+        for (int r = 0; r < SR; r += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(subs + r);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const int at = (r >> 1) + a;
+            const float2 x2 = __ffma2_rn(make_float2(v[2 * at], v[2 * at + 1]), make_float2(p.c, p.c),
+                                         a ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+            const float2 pr = make_float2(ex2f(x2.x), ex2f(x2.y));
+            l[at] = __fadd2_rn(l[at], pr);
+            w[at] = pack16(pr.x, pr.y, T());
+            if constexpr (kLo)
+              e[at] = pack16(pr.x - __uint_as_float(w[at] << 16), pr.y - __uint_as_float(w[at] & 0xffff0000u), T());
+          }
+        }
         // the buffer of P: with one, the last product must have read it; with
         // two, these scores came behind the product that read it
         if (C::kPBufs == 1 && n_s > 0) ok = ok && last_product();
         uint8_t *dst = smem + C::kP + n_s % C::kPBufs * C::kPBytes + (row0 >> 3) * (kTile * 16) + t * 16;
 #pragma unroll
-        for (int g = 0; g < SR; g += 8) {
-          uint32_t w[4], e[4];
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(refs + g + j);
-            const float fr[4] = {f.x, f.y, f.z, f.w};
-            float pr[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              const float sub = fr[a] == -INFINITY ? 0.f : fr[a] - kShift<T>;
-              pr[a] = ex2f(fmaf(v[g + j + a], p.c, -sub));
-              l[g + j + a] += pr[a];
-            }
-            w[j >> 1] = pack16(pr[0], pr[1], T());
-            w[(j >> 1) + 1] = pack16(pr[2], pr[3], T());
-            if constexpr (kLo) {
-#pragma unroll
-              for (int a = 0; a < 2; ++a)
-                e[(j >> 1) + a] = pack16(pr[2 * a] - __uint_as_float(w[(j >> 1) + a] << 16),
-                                         pr[2 * a + 1] - __uint_as_float(w[(j >> 1) + a] & 0xffff0000u), T());
-            }
-          }
-          *reinterpret_cast<uint4 *>(dst + (g >> 3) * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int g = 0; g < SR / 8; ++g) {
+          *reinterpret_cast<uint4 *>(dst + g * (kTile * 16)) = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
           if constexpr (kLo)
-            *reinterpret_cast<uint4 *>(dst + ((NR + g) >> 3) * (kTile * 16)) = make_uint4(e[0], e[1], e[2], e[3]);
+            *reinterpret_cast<uint4 *>(dst + (NR / 8 + g) * (kTile * 16)) =
+                make_uint4(e[4 * g], e[4 * g + 1], e[4 * g + 2], e[4 * g + 3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
@@ -1314,7 +1317,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
       side_sync(x);  // the maxima of a last move have been read
 #pragma unroll
       for (int r = 0; r < SR; ++r) {
-        float a = l[r];
+        float a = r & 1 ? l[r >> 1].y : l[r >> 1].x;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         if (lane == 0) part[(warp & 3) * SR + r] = a;
@@ -1326,7 +1329,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
         factor[t] = !s.whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
         if (!s.whole && row0 + t < p.R)
           *reinterpret_cast<float2 *>(rec + 2 * (row0 + t)) =
-              make_float2(refs[t] == -INFINITY ? -INFINITY : refs[t] - kShift<T>, sum);
+              make_float2(refs[t] - kShift<T>, sum);
       }
       ok = ok && last_product();
       tc_fence_after();
@@ -1464,9 +1467,10 @@ void row_tiles(Attend16 &p, int group) {
 
 // a kernel's launch with its dynamic shared memory
 template <typename... P, typename... A>
-cudaError_t launch_tiles(void (*kernel)(P...), int smem, unsigned grid, cudaStream_t stream, const A &...args) {
+cudaError_t launch_tiles(void (*kernel)(P...), int threads, int smem, unsigned grid, cudaStream_t stream,
+                         const A &...args) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(kThreads16), smem, stream, args...);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
 }
 int rows_smem(const Attend16 &p) { return 4 * p.q_half + p.slots * kTileBytes + kOffMl + kTile * 8; }
 
@@ -1474,7 +1478,7 @@ template <typename T, int NR>
 cudaError_t launch_cols(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid, cudaStream_t stream) {
   p.slots = Cols<T, NR>::kSlots;
   p.q_half = Cols<T, NR>::kQBytes / 2;
-  return launch_tiles(k_cols16<T, NR>, Cols<T, NR>::kBytes, grid, stream, p, mq, mk);
+  return launch_tiles(k_cols16<T, NR>, Cols<T, NR>::kThreads, Cols<T, NR>::kBytes, grid, stream, p, mq, mk);
 }
 template <typename T>
 cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid,
@@ -1484,7 +1488,7 @@ cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &m
   if (p.R <= 64) return launch_cols<T, 64>(p, mq, mk, grid, stream);
   p.slots = 5;
   p.q_half = kTileBytes / 2;
-  return launch_tiles(k_attend16<T, true>, rows_smem(p), grid, stream, p, mq, mk, mk);
+  return launch_tiles(k_attend16<T, true>, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
 }
 
 // the cache's row tiles: rows, and the stride of a record's rows
@@ -1527,8 +1531,8 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(grid);
   return dtype == ISOQUANT_BF16
-             ? launch_tiles(k_attend16<__nv_bfloat16, false>, rows_smem(p), g, stream, p, mq, mk, mv)
-             : launch_tiles(k_attend16<__half, false>, rows_smem(p), g, stream, p, mq, mk, mv);
+             ? launch_tiles(k_attend16<__nv_bfloat16, false>, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv)
+             : launch_tiles(k_attend16<__half, false>, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv);
 }
 
 size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s) {
