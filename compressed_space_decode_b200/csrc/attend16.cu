@@ -519,6 +519,7 @@ __device__ void drain(const Attend16 &p, const Ring &ring, Bars &bars, bool ok) 
   }
 }
 
+constexpr int kBox = 32;
 // The loader warp over the cache: key and value tiles in the order of their
 // use, K0 K1 V0 K2 V1 .., and the segments' queries into q_bufs buffers whose
 // 64-dim halves are p.q_half bytes.
@@ -539,8 +540,8 @@ __device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensor
     }
     __syncwarp();
     const int end = none_sees(p, s, p.tok);
-    const int box = min(kTile, 1 << p.ps_shift), boxes = kTile / box;
-    // lane 2 i + hf loads half hf of the tile's i-th page
+    // lane 2 i + hf loads half hf of the tile's i-th box
+    constexpr int box = kBox, boxes = kTile / box;
     const int hf = lane & 1, part = lane >> 1;
     auto page_of = [&](int i) {  // this lane's page of tile i: -1 if nothing of it is seen, -2 if it is none
       const int t = (s.j0 + i) * kTile + part * box;
@@ -1041,7 +1042,8 @@ struct Cols {
   static constexpr int kN = kLo ? 2 * NR : NR;         // columns of O^T
   static constexpr int kQBufs = NR == 64 ? 1 : 2;
   static constexpr int kPBufs = NR == 64 ? 1 : 2;
-  static constexpr int kSlots = NR == 16 ? 6 : 5;
+  // 16 x 32768 tokens: 4 slots 186 us, 5 186, 6 200; 4 long contexts: 246, 260, 272
+  static constexpr int kSlots = 4;
   static constexpr int kQBytes = NR * kD * 2;
   static constexpr int kPBytes = kN * kTile * 2;
   static constexpr int kP = kQBufs * kQBytes;
@@ -1567,7 +1569,7 @@ cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_ca
   const int64_t rows = static_cast<int64_t>(cache->num_pages) * 2 * p.H * cache->page_size;
   const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {kD * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(cache->page_size < kTile ? cache->page_size : kTile)};
+  const cuuint32_t box[2] = {64, kBox};
   if (!encode_rows(&mq, cache->dtype, q, static_cast<int64_t>(s.batch) * s.nq, p.Hq,
                    static_cast<int64_t>(p.Hq) * kD, p.GB, p.tok) ||
       !encode(&mk, cache->dtype, 2, cache->data, dims, strides, box))
