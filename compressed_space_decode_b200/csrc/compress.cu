@@ -205,37 +205,56 @@ __device__ __forceinline__ void sign_a(const uint32_t (&sgn)[8], float2 (&a)[8])
     a[m].y = __uint_as_float(__float_as_uint(a[m].y) ^ (sgn[m] & 0x80000000u));
   }
 }
-// The position rotation of a layout-A lane's coordinates by table row `row`:
-// HM = rot / 32 rows m of the pair's first coordinates.  fp32: a c - fl(b s)
-// in one fma, so the rotated vector is off by at most 2 * 2^-24 of its norm.
+// A layout-A lane's part of a table row: the cosines and sines of its pairs
+// (16m + 2q and 16m + 2q + 1 of the first half, m < rot / 32; interleaved:
+// pair 8m + q, m < rot / 16, two per float2).
+struct RopeLane {
+  float2 c[4], s[4];
+};
+__device__ __forceinline__ void load_rope(const RopeArgs &r, int64_t pos, int q, RopeLane &t) {
+  const float *row = r.table + pos * r.rot;
+  const int half = r.rot >> 1;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    if (32 * m < r.rot) {
+      if (r.inter) {
+        t.c[m] = make_float2(row[16 * m + q], row[16 * m + 8 + q]);
+        t.s[m] = make_float2(row[half + 16 * m + q], row[half + 16 * m + 8 + q]);
+      } else {
+        t.c[m] = *reinterpret_cast<const float2 *>(row + 16 * m + 2 * q);
+        t.s[m] = *reinterpret_cast<const float2 *>(row + half + 16 * m + 2 * q);
+      }
+    }
+  }
+}
+// The position rotation of a layout-A lane's coordinates, HM = rot / 32.
+// fp32: a c - fl(b s) in one fma, so the rotated vector is off by at most
+// 2 * 2^-24 of its norm.
 template <int HM>
-__device__ __forceinline__ void rope_a_rot(const float *row, int q, int inter, float2 (&a)[8]) {
+__device__ __forceinline__ void rope_a_rot(const RopeLane &t, int inter, float2 (&a)[8]) {
   if (inter) {
 #pragma unroll
     for (int m = 0; m < 2 * HM; ++m) {
-      const float c = row[8 * m + q], s = row[16 * HM + 8 * m + q];
-      const float2 t = a[m];
-      a[m].x = fmaf(t.x, c, -(t.y * s));
-      a[m].y = fmaf(t.y, c, t.x * s);
+      const float c = m & 1 ? t.c[m >> 1].y : t.c[m >> 1].x, s = m & 1 ? t.s[m >> 1].y : t.s[m >> 1].x;
+      const float2 v = a[m];
+      a[m].x = fmaf(v.x, c, -(v.y * s));
+      a[m].y = fmaf(v.y, c, v.x * s);
     }
     return;
   }
 #pragma unroll
   for (int m = 0; m < HM; ++m) {
-    const float2 c = *reinterpret_cast<const float2 *>(row + 16 * m + 2 * q);
-    const float2 s = *reinterpret_cast<const float2 *>(row + 16 * HM + 16 * m + 2 * q);
-    const float2 lo = a[m], hi = a[m + HM];
+    const float2 c = t.c[m], s = t.s[m], lo = a[m], hi = a[m + HM];
     a[m] = __ffma2_rn(lo, c, __fmul2_rn(hi, make_float2(-s.x, -s.y)));
     a[m + HM] = __ffma2_rn(hi, c, __fmul2_rn(lo, s));
   }
 }
-__device__ __forceinline__ void rope_a(const RopeArgs &r, int64_t pos, int q, float2 (&a)[8]) {
-  const float *row = r.table + pos * r.rot;
+__device__ __forceinline__ void rope_a(const RopeArgs &r, const RopeLane &t, float2 (&a)[8]) {
   switch (r.rot) {
-    case 32: rope_a_rot<1>(row, q, r.inter, a); break;
-    case 64: rope_a_rot<2>(row, q, r.inter, a); break;
-    case 96: rope_a_rot<3>(row, q, r.inter, a); break;
-    default: rope_a_rot<4>(row, q, r.inter, a); break;
+    case 32: rope_a_rot<1>(t, r.inter, a); break;
+    case 64: rope_a_rot<2>(t, r.inter, a); break;
+    case 96: rope_a_rot<3>(t, r.inter, a); break;
+    default: rope_a_rot<4>(t, r.inter, a); break;
   }
 }
 
@@ -466,9 +485,13 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
   // ahead, so that their latency overlaps the current vector's rotation
   RawA<T> nraw{};
   int64_t nslot = -1, npos = 0;
+  RopeLane nrope{};
   if (t_begin + grp < t_end) {
     nslot = g.slots[t_begin + grp];
-    if constexpr (ROPE) npos = r.k_pos[t_begin + grp];
+    if constexpr (ROPE) {
+      npos = r.k_pos[t_begin + grp];
+      if (kv == 0 && nslot >= 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
+    }
     load_a(src + (static_cast<int64_t>(t_begin + grp) * H + h) * kD, q, nraw);
   }
   for (int tb = t_begin; tb < t_end; tb += 4) {
@@ -487,7 +510,7 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
         if (kv == 0) {
           const uint32_t none[8] = {};
           unpack_a(nraw, none, a);
-          if (slot >= 0) rope_a(r, pos, q, a);
+          if (slot >= 0) rope_a(r, nrope, a);
           sign_a(lc.sgn, a);
         } else {
           unpack_a(nraw, lc.sgn, a);
@@ -501,7 +524,10 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
     }
     if (t + 4 < t_end) {
       nslot = g.slots[t + 4];
-      if constexpr (ROPE) npos = r.k_pos[t + 4];
+      if constexpr (ROPE) {
+        npos = r.k_pos[t + 4];
+        if (kv == 0 && nslot >= 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
+      }
       load_a(src + (static_cast<int64_t>(t + 4) * H + h) * kD, q, nraw);
     }
     const int64_t page = slot >> ps_shift;
@@ -703,14 +729,12 @@ struct RotateArgs {
   const void *q;
   int n_rows, Hq, G;
   float *out;
+  uint32_t strip;  // rotate_strip: vectors per warp (a multiple of 4)
 };
 
 // q_rot = R q for query vector `vec` (row vec / Hq, head vec % Hq).
-// ROPE: q is rotated by position first; a row whose position is outside the
-// table is written as zeros.
-template <typename T, bool ROPE = false>
-__device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, int lane,
-                                            const RopeArgs &r = RopeArgs{}, uint32_t *status = nullptr) {
+template <typename T>
+__device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, int lane) {
   const HeadParams *__restrict__ params = g.params;
   const T *__restrict__ q = static_cast<const T *>(g.q);
   const int n_rows = g.n_rows, Hq = g.Hq, G = g.G;
@@ -719,19 +743,6 @@ __device__ __forceinline__ void rotate_warp(const RotateArgs &g, uint32_t vec, i
   const int hq = static_cast<int>(vec % static_cast<uint32_t>(Hq));
   float x[4], y[4];
   load4(q + static_cast<int64_t>(vec) * kD + 4 * lane, x);
-  if constexpr (ROPE) {
-    const int64_t pos = r.q_pos[vec / static_cast<uint32_t>(Hq)];
-    if (pos < 0 || pos >= r.num_pos) {
-      if (lane == 0) set_status(status, ISOQUANT_DEVERR_POS_RANGE);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = 0.f;
-    } else {
-      float xr[4];
-      rope4(r, pos, lane, x, xr);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = xr[i];
-    }
-  }
   rotate_f32(params[hq / G], lane, x, y);
   const float s = 0.08838834764831845f;  // 1/sqrt(128): the normalisation of Hn
   *reinterpret_cast<float4 *>(out + static_cast<int64_t>(vec) * kD + 4 * lane) = make_float4(y[0] * s, y[1] * s, y[2] * s, y[3] * s);
@@ -763,11 +774,77 @@ __global__ void __launch_bounds__(256) k_decode_prep(const CompressArgs c, const
   }
 }
 
-// k_decode_prep with the position rotation in both halves.
+// k_decode_prep with the position rotation in both halves.  Queries go four
+// vectors at a time through the two layouts of the compress path: strips of
+// g.strip of a KV head's (row, group head) vectors, so that the head's SO(4)
+// blocks are loaded once.  8192 rows of 32 heads: 412 us with one warp per
+// vector as in k_decode_prep, 65 us so (201 MB; instruction issue bounds it).
+// The result's 64 bytes per lane go out as two 32-byte stores (whole sectors).
+__device__ __forceinline__ void store8(float *dst, const float *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t w, int lane, float *tile,
+                                             const RopeArgs &r, uint32_t *status) {
+  const uint32_t H = static_cast<uint32_t>(g.Hq / g.G), total = static_cast<uint32_t>(g.n_rows) * g.G;
+  const uint32_t sidx = w / H;
+  const int h = static_cast<int>(w - sidx * H);
+  const uint32_t begin = sidx * g.strip;
+  if (begin >= total) return;
+  const uint32_t end = min(begin + g.strip, total);
+  const int grp = lane >> 3, q = lane & 7;
+  LaneConsts lc;
+  lane_consts(g.params[h], q, lc);
+  const T *__restrict__ src = static_cast<const T *>(g.q) + static_cast<int64_t>(h) * g.G * kD;
+  float *__restrict__ dst = g.out + static_cast<int64_t>(h) * g.G * kD + 16 * q;
+  const bool wide = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0;
+  // the next vector's inputs and table row are loaded one iteration ahead
+  RawA<T> raw{};
+  RopeLane rope{};
+  uint32_t row = 0, head = 0;  // of the vector in hand
+  bool good = false;
+  auto fetch = [&](uint32_t e) {
+    row = e / static_cast<uint32_t>(g.G);
+    head = e - row * g.G;
+    const int64_t pos = r.q_pos[row];
+    good = pos >= 0 && pos < r.num_pos;
+    if (good) load_rope(r, pos, q, rope);
+    else if (q == 0) set_status(status, ISOQUANT_DEVERR_POS_RANGE);
+    load_a(src + (static_cast<int64_t>(row) * g.Hq + head) * kD, q, raw);
+  };
+  if (begin + grp < end) fetch(begin + grp);
+  for (uint32_t e0 = begin; e0 < end; e0 += 4) {
+    const uint32_t e = e0 + grp;
+    const bool live = e < end, zero = !good;
+    float *o = dst + (static_cast<int64_t>(row) * g.Hq + head) * kD;
+    float2 a[8];
+    const uint32_t none[8] = {};
+    unpack_a(raw, none, a);
+    rope_a(r, rope, a);
+    sign_a(lc.sgn, a);
+    if (e + 4 < end) fetch(e + 4);
+    float y[16];
+    rotate_two_layouts(a, lc, tile, grp, q, y);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = zero ? 0.f : y[i] * 0.08838834764831845f;  // Hn = H / sqrt(128)
+      if (wide) {
+        store8(o, y);
+        store8(o + 8, y + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+      }
+    }
+  }
+}
+
 template <typename T, int BITS>
-__global__ void __launch_bounds__(256) k_decode_prep_rope(const CompressArgs c, const RotateArgs r,
-                                                          const RopeArgs rope, int nbc) {
-  __shared__ __align__(16) float tile[8][kTileFloats];
+__global__ void __launch_bounds__(kCompressWarps * 32, kCompressBlocksPerSm)
+    k_decode_prep_rope(const CompressArgs c, const RotateArgs r, const RopeArgs rope, int nbc) {
+  __shared__ __align__(16) float tile[kCompressWarps][kTileFloats];
   pdl_trigger();
   pdl_wait();
   const uint32_t warp = threadIdx.x >> 5;
@@ -775,10 +852,10 @@ __global__ void __launch_bounds__(256) k_decode_prep_rope(const CompressArgs c, 
   const int bx = static_cast<int>(blockIdx.x);
   if (bx < 2 * nbc) {
     const int kv = bx >= nbc ? 1 : 0;
-    compress_warp<T, BITS, true>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * (blockDim.x >> 5) + warp, lane,
-                                 tile[warp], rope);
+    compress_warp<T, BITS, true>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * kCompressWarps + warp, lane, tile[warp],
+                                 rope);
   } else {
-    rotate_warp<T, true>(r, static_cast<uint32_t>(bx - 2 * nbc) * (blockDim.x >> 5) + warp, lane, rope, c.status);
+    rotate_strip<T>(r, static_cast<uint32_t>(bx - 2 * nbc) * kCompressWarps + warp, lane, tile[warp], rope, c.status);
   }
 }
 
@@ -950,15 +1027,21 @@ cudaError_t launch_decode_prep_rope(const isoquant_ctx *ctx, const isoquant_cach
                                     const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
                                     const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
                                     const isoquant_rope *rope, float *q_rot, cudaStream_t stream) {
-  const int64_t nbc = compress_blocks(ctx, n_tok, 8);
-  const int64_t nbr = rotate_blocks(n_rows, num_q_heads);
+  const int64_t nbc = compress_blocks(ctx, n_tok, kCompressWarps);
+  const CompressArgs c = compress_args(ctx, cache, k, v, n_tok, slot_mapping);
+  RotateArgs r = rotate_args(ctx, q, n_rows, num_q_heads, q_rot);
+  // as many strips as the SMs hold warps, of 4 to 64 vectors
+  const int64_t vectors = static_cast<int64_t>(n_rows) * num_q_heads;
+  const int64_t resident = static_cast<int64_t>(ctx->num_sms) * kCompressWarps * kCompressBlocksPerSm;
+  const int64_t even = (vectors / resident) & ~int64_t(3);
+  r.strip = static_cast<uint32_t>(even < 4 ? 4 : even > 64 ? 64 : even);
+  const int64_t strips = (static_cast<int64_t>(n_rows) * r.G + r.strip - 1) / r.strip * ctx->num_kv_heads;
+  const int64_t nbr = (strips + kCompressWarps - 1) / kCompressWarps;
   const int64_t blocks = 2 * nbc + nbr;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const CompressArgs c = compress_args(ctx, cache, k, v, n_tok, slot_mapping);
-  const RotateArgs r = rotate_args(ctx, q, n_rows, num_q_heads, q_rot);
   const RopeArgs ra{rope->cos_sin, k_pos, q_pos, rope->num_positions, rope->rot_dim, rope->interleaved};
-  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kCompressWarps * 32);
   const int nb = static_cast<int>(nbc);
   switch (ctx->codebook.bits) {
     case 2: return launch_prep_rope_t<2>(dtype, grid, block, stream, c, r, ra, nb);
