@@ -46,12 +46,15 @@ namespace {
 constexpr int kTile = 128;                  // rows of a row tile, tokens of a key tile
 constexpr int kTileBytes = kTile * kD * 2;  // 32 KB
 constexpr int kMaxSlots = 6;
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kGuardWarp = 2;  // and 3; then the sides' softmax warps
+// warps 0 and 1 issue products, then these, then the sides' softmax warps
+constexpr int kLoadWarp = 2, kGuardWarp = 3;
+constexpr int kKeySlots = 2;                // of a ring; the others hold values
+constexpr int kRowSlots = 5;                // of k_attend16
 constexpr int kThreads16 = 3 * 128;         // k_attend16: two sides
 // shared memory behind the tiles
 constexpr int kOffBad = 0;                      // first token with +inf, -inf, NaN of each dim
 constexpr int kOffBar = kOffBad + 3 * kD * 4;   // barriers
-constexpr int kOffFlags = kOffBar + 256;
+constexpr int kOffFlags = kOffBar + 320;
 constexpr int kOffLoc = kOffFlags + 16;         // the CTA's part, then locate's scratch
 constexpr int kTailBytes = kOffLoc + 160;
 constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (reference, sum) of each row
@@ -119,18 +122,22 @@ __device__ constexpr uint32_t idesc16(int n, int a_mn, int b_mn) {
   return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) |
          (static_cast<uint32_t>(b_mn) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// (the whole warp runs the issuing code, so that its descriptors stay in
+// uniform registers; the thread with `issue` set issues)
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
       : "memory");
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -160,59 +167,77 @@ constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
 template <typename T, bool kLo>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int vis, bool first, float &ref,
                                              float &l) {
-  float s[4][32];
+  constexpr float kMost = kShift<T> == 0.f ? 256.f : 32768.f;  // 2^(8 + shift)
+  const float2 c2 = make_float2(c, c);
+  float sum;
+  uint32_t w[64], e[kLo ? 64 : 1];
+  bool move = first || (ref == -INFINITY && vis > 0), moved = move, again = __any_sync(0xffffffffu, move);
+  while (true) {
+    float s[4][32];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) tmem_ld32_async(ts + 32 * k, s[k]);
+    for (int k = 0; k < 4; ++k) tmem_ld32_async(ts + 32 * k, s[k]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) tmem_arrived(s[k]);
-  if (__any_sync(0xffffffffu, vis < kTile)) {
+    for (int k = 0; k < 4; ++k) tmem_arrived(s[k]);
+    if (__any_sync(0xffffffffu, vis < kTile)) {
 #pragma unroll
-    for (int i = 0; i < kTile; ++i)
-      if (i >= vis) s[i >> 5][i & 31] = -INFINITY;
-  }
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      for (int i = 0; i < kTile; ++i)
+        if (i >= vis) s[i >> 5][i & 31] = -INFINITY;
+    }
+    if (again) {
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < kTile; i += 8) {
+      for (int i = 0; i < kTile; i += 8) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], s[i >> 5][(i + e) & 31], s[i >> 5][(i + e + 4) & 31]);
-  }
-  const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * c;
-  const bool move = !(mt <= ref + kLazy);  // a NaN moves too
-  if (__any_sync(0xffffffffu, move)) {
-    const float to_ref = move ? mt : ref;
-    const float corr = move ? ex2f(ref - to_ref) : 1.f;
-    ref = to_ref;
-    l *= corr;
-    if (!first) {
+        for (int j = 0; j < 4; ++j) mx[j] = max3_nan(mx[j], s[i >> 5][(i + j) & 31], s[i >> 5][(i + j + 4) & 31]);
+      }
+      const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * c;
+      const bool up = move && !(mt <= ref);
+      const float corr = up ? ex2f(ref - mt) : 1.f;
+      if (up) ref = mt;
+      l *= corr;
+      if (!first) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float o[32];
-        tmem_ld32(to + 32 * k, o);
+        for (int k = 0; k < 4; ++k) {
+          float o[32];
+          tmem_ld32(to + 32 * k, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= corr;
-        tmem_st32(to + 32 * k, o);
+          for (int i = 0; i < 32; ++i) o[i] *= corr;
+          tmem_st32(to + 32 * k, o);
+        }
       }
     }
+    // (NaN for a NaN or +inf)
+    const float sub = ref == -INFINITY ? 0.f : (ref - kShift<T>) + (ref - ref);
+    const float2 n2 = make_float2(-sub, -sub);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < kTile; i += 2) {
+      const float2 y = __ffma2_rn(make_float2(s[i >> 5][i & 31], s[i >> 5][(i & 31) + 1]), c2, n2);
+      const float2 p = make_float2(ex2f(y.x), ex2f(y.y));
+      part[(i >> 1) & 1] = __fadd2_rn(part[(i >> 1) & 1], p);
+      const uint32_t hi = pack16(p.x, p.y, T());
+      w[i >> 1] = hi;
+      if constexpr (kLo) e[i >> 1] = pack16(p.x - __uint_as_float(hi << 16), p.y - __uint_as_float(hi & 0xffff0000u), T());
+    }
+    sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+    move = !moved && !(sum <= kMost);  // a NaN moves too
+    moved |= move;
+    again = __any_sync(0xffffffffu, move);
+    if (!again) break;
   }
-  const float sub = ref == -INFINITY ? 0.f : ref - kShift<T>;
-  const float2 c2 = make_float2(c, c), n2 = make_float2(-sub, -sub);
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  l += sum;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t w[16], r[16];
+    uint32_t part[16];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 x = __ffma2_rn(make_float2(s[k][i], s[k][i + 1]), c2, n2);
-      const float2 p = make_float2(ex2f(x.x), ex2f(x.y));
-      sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
-      w[i >> 1] = pack16(p.x, p.y, T());
-      if constexpr (kLo)
-        r[i >> 1] = pack16(p.x - __uint_as_float(w[i >> 1] << 16), p.y - __uint_as_float(w[i >> 1] & 0xffff0000u), T());
+    for (int i = 0; i < 16; ++i) part[i] = w[16 * k + i];
+    tmem_st16u(ts + 16 * k, part);
+    if constexpr (kLo) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[i] = e[16 * k + i];
+      tmem_st16u(ts + 64 + 16 * k, part);
     }
-    tmem_st16u(ts + 16 * k, w);
-    if constexpr (kLo) tmem_st16u(ts + 64 + 16 * k, r);
   }
-  l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
   tmem_stored();
 }
 
@@ -415,63 +440,59 @@ __device__ __forceinline__ uint32_t exponent_mask() {
   return std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
 }
 
-// The barriers of a CTA: ring slots filled and freed, queries there and used,
-// a side's scores, weights and last product, then the guards' (guarded, go,
-// cleared) and the sides' hand-overs.
+// The barriers of a CTA: ring slots filled (for a tile that the guard sees to
+// first: loaded), freed; queries there and used; a side's or tile's scores
+// there and read, weights, products; the sides' hand-overs; all products.
 struct Bars {
-  uint64_t full[kMaxSlots], freed[kMaxSlots], q_full[2], q_free[2], s_full[2], p_full[2], o_done[2];
-  uint64_t guarded, go, cleared, side1, seg_done, mma_done;
-  __device__ void init(int p_count, int seg_count) {
+  uint64_t full[kMaxSlots], loaded[kMaxSlots], freed[kMaxSlots];
+  uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], o_done[2], turn[2], side1, seg_done, mma_done;
+  // arrivals: freed and q_free take `users`, the weights p_count and a segment's end seg_count
+  __device__ void init(int slot_users, int q_users, int p_count, int seg_count) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&freed[i], 1);
+      mbar_init(&loaded[i], 1);
+      mbar_init(&freed[i], slot_users);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_free[i], 1);
+      mbar_init(&q_free[i], q_users);
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], p_count);
       mbar_init(&p_full[i], p_count);
       mbar_init(&o_done[i], 1);
+      mbar_init(&turn[i], 1);
     }
-    mbar_init(&guarded, 2);
-    mbar_init(&go, 1);
-    mbar_init(&cleared, 1);
     mbar_init(&side1, seg_count);
     mbar_init(&seg_done, seg_count);
-    mbar_init(&mma_done, 1);
+    mbar_init(&mma_done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
-static_assert(sizeof(Bars) <= 256, "room for the barriers");
+static_assert(sizeof(Bars) <= 320, "room for the barriers");
 // what the roles of a CTA share beside the barriers
 struct Flags {
   uint32_t tmem;
-  int abort, issued, nonfinite;
+  int abort;
+  int nonfinite;  // the segment, counted from 1, that the guard's marks belong to
+  int done;       // softmax warps' ends of segments
 };
 
-// the next ring slot in the order of use, and how often it was used before
-struct Ring {
-  uint32_t slot = 0, round = 0;
-  int slots;
-  __device__ explicit Ring(int n) : slots(n) {}
-  __device__ uint32_t step() {
-    const uint32_t s = slot;
-    if (++slot == static_cast<uint32_t>(slots)) {
-      slot = 0;
-      ++round;
-    }
-    return s;
-  }
-};
+// The ring: tile t's keys lie in slot t mod kKeySlots, its values in one of the
+// other slots in turn.  use: how often the slot was used before.
+__device__ __forceinline__ uint32_t key_slot(uint32_t t) { return t % kKeySlots; }
+__device__ __forceinline__ uint32_t key_use(uint32_t t) { return t / kKeySlots; }
+__device__ __forceinline__ uint32_t value_slot(uint32_t t, int slots) { return kKeySlots + t % (slots - kKeySlots); }
+__device__ __forceinline__ uint32_t value_use(uint32_t t, int slots) { return t / (slots - kKeySlots); }
 
 __device__ __forceinline__ float *record(const Attend16 &p, int i) {
   return p.records + i * (static_cast<int64_t>(p.row_stride) * (kD + 2));
 }
 
-// Tensor memory of COLS columns, the barriers and the guards' marks; the
+// Tensor memory of COLS columns, the barriers and the guard's marks; the
 // caller's next __syncthreads makes them visible.
 template <uint32_t COLS>
-__device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, int p_count, int seg_count) {
+__device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, int slot_users, int q_users,
+                                          int p_count, int seg_count) {
   if (threadIdx.x < 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&flags->tmem)),
                  "r"(COLS));
@@ -479,8 +500,8 @@ __device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, in
     tc_fence_before();
   }
   if (threadIdx.x == 32) {
-    bars.init(p_count, seg_count);
-    flags->abort = flags->issued = flags->nonfinite = 0;
+    bars.init(slot_users, q_users, p_count, seg_count);
+    flags->abort = flags->nonfinite = flags->done = 0;
   }
   for (int i = threadIdx.x; i < 3 * kD; i += blockDim.x) bad[i] = INT_MAX;
 }
@@ -490,7 +511,7 @@ __device__ __forceinline__ void end_cta(Bars &bars, Flags *flags, const Attend16
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x < 32) {
-    if (*const_cast<volatile int *>(&flags->issued)) mbar_wait(&bars.mma_done, 0, p.status, nullptr);
+    mbar_wait(&bars.mma_done, 0, p.status, nullptr);
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(flags->tmem), "r"(COLS));
   }
@@ -510,28 +531,51 @@ __device__ __forceinline__ int none_sees(const Attend16 &p, const Segment &s, in
   return s.limit(min(s.rows, s.row0 + tokens) - 1, p.causal);
 }
 
-// Before a CTA that gave up ends: waits for the copies of each slot's last use.
-__device__ void drain(const Attend16 &p, const Ring &ring, Bars &bars, bool ok) {
-  if (ok) return;
-  for (uint32_t i = 0; i < static_cast<uint32_t>(p.slots); ++i) {
-    const uint32_t used = ring.round + (i < ring.slot ? 1u : 0u);
-    if (used > 0) mbar_wait(&bars.full[i], (used - 1) & 1u, p.status, nullptr);
+// The loader warp's ring: begin() waits until a slot is free and says which
+// barrier the tile's copies complete on.
+struct Loader {
+  const Attend16 &p;
+  Bars &bars;
+  volatile int *abort;
+  bool ok = true;
+  // lane i: slot i's uses, those that the guard sees to, and whether the last was one
+  uint32_t uses = 0, guards = 0;
+  bool guarded = false;
+  __device__ Loader(const Attend16 &p_, Bars &b, volatile int *a) : p(p_), bars(b), abort(a) {}
+  __device__ uint64_t *begin(uint32_t slot, uint32_t use, bool guard, uint32_t bytes) {
+    if (use > 0) ok = ok && warp_wait(&bars.freed[slot], (use - 1) & 1u, p, abort);
+    if (!ok) return nullptr;
+    const uint32_t lane = threadIdx.x & 31;
+    uint64_t *bar = guard ? &bars.loaded[slot] : &bars.full[slot];
+    if (lane == slot) {
+      guarded = guard;
+      ++uses;
+      guards += guard;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    __syncwarp();
+    return bar;
   }
-}
+  // before a CTA that gave up ends: waits for the copies
+  __device__ void drain() {
+    const uint32_t lane = threadIdx.x & 31, n = guarded ? guards : uses;
+    if (!ok && n > 0) mbar_wait(guarded ? &bars.loaded[lane] : &bars.full[lane], (n - 1) & 1u, p.status, nullptr);
+    __syncwarp();
+  }
+};
 
 constexpr int kBox = 32;
-// The loader warp over the cache: key and value tiles in the order of their
-// use, K0 K1 V0 K2 V1 .., and the segments' queries into q_bufs buffers whose
-// 64-dim halves are p.q_half bytes.
+// The loader warp over the cache: the segments' queries into q_bufs buffers
+// whose 64-dim halves are p.q_half bytes, key and value tiles into the ring.
 __device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensorMap &mq, const CUtensorMap &mk,
                            uint32_t sq, uint32_t sr, int q_bufs, Bars &bars, volatile int *abort) {
   const int lane = threadIdx.x & 31;
-  Ring ring(p.slots);
-  bool ok = true;
+  Loader ld(p, bars, abort);
+  uint32_t t = 0;  // tiles so far
   cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
     const uint32_t qb = k % q_bufs, use = k / q_bufs;
-    if (use > 0) ok = ok && warp_wait(&bars.q_free[qb], (use - 1) & 1u, p, abort);
-    if (lane == 0 && ok) {
+    if (use > 0) ld.ok = ld.ok && warp_wait(&bars.q_free[qb], (use - 1) & 1u, p, abort);
+    if (lane == 0 && ld.ok) {
       mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(p.R * kD * 2));
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
@@ -539,131 +583,126 @@ __device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensor
                &bars.q_full[qb]);
     }
     __syncwarp();
-    const int end = none_sees(p, s, p.tok);
+    const int end = none_sees(p, s, p.tok), all = all_see(p, s);
     // lane 2 i + hf loads half hf of the tile's i-th box
     constexpr int box = kBox, boxes = kTile / box;
     const int hf = lane & 1, part = lane >> 1;
     auto page_of = [&](int i) {  // this lane's page of tile i: -1 if nothing of it is seen, -2 if it is none
-      const int t = (s.j0 + i) * kTile + part * box;
-      if (i >= s.n[0] || part >= boxes || t >= end) return -1;
-      const int page = p.page_table[static_cast<int64_t>(s.b) * p.max_pages + (t >> p.ps_shift)];
+      const int at = (s.j0 + i) * kTile + part * box;
+      if (i >= s.n[0] || part >= boxes || at >= end) return -1;
+      const int page = p.page_table[static_cast<int64_t>(s.b) * p.max_pages + (at >> p.ps_shift)];
       return page < 0 || page >= p.num_pages ? -2 : page;
     };
-    int pages[3] = {-1, -1, -1};  // of tiles i, i - 1, i - 2
     int ahead = page_of(0);
-    for (int i = 0; i < s.n[0] + 2 && ok; ++i) {
-      pages[2] = pages[1];
-      pages[1] = pages[0];
-      pages[0] = ahead;
+    for (int i = 0; i < s.n[0] && ld.ok; ++i, ++t) {
+      int page = ahead;
       ahead = page_of(i + 1);
-      if (pages[0] == -2) {
+      if (page == -2) {
         set_status(p.status, ISOQUANT_DEVERR_PAGE_RANGE);
-        pages[0] = 0;
+        page = 0;
       }
-      auto load = [&](int page, int tile, int kv) {
-        if (ring.round > 0) ok = ok && warp_wait(&bars.freed[ring.slot], (ring.round - 1) & 1u, p, abort);
-        if (!ok) return;
-        const uint32_t sl = ring.step();
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128u;
-        if (lane == 0) mbar_arrive_expect_tx(&bars.full[sl], bytes);
-        __syncwarp();
-        if (page >= 0) {
-          const int off = ((s.j0 + tile) * kTile + part * box) & ((1 << p.ps_shift) - 1);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128u;
+      const int t0 = (s.j0 + i) * kTile;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t sl = kv ? value_slot(t, p.slots) : key_slot(t);
+        uint64_t *bar = ld.begin(sl, kv ? value_use(t, p.slots) : key_use(t), kv && t0 + kTile > all, bytes);
+        if (page >= 0 && ld.ok) {
           // one row per token: below 2^31 rows, checked on the host
+          const int off = (t0 + part * box) & ((1 << p.ps_shift) - 1);
           const int row = ((page * 2 + kv) * p.H + s.h) * (1 << p.ps_shift) + off;
-          tma_2d(sr + sl * kTileBytes + hf * (kTileBytes / 2) + part * box * 128, &mk, 64 * hf, row, &bars.full[sl]);
+          tma_2d(sr + sl * kTileBytes + hf * (kTileBytes / 2) + part * box * 128, &mk, 64 * hf, row, bar);
         }
         __syncwarp();
-      };
-      if (i >= 2 && i - 2 < s.n[0]) load(pages[2], i - 2, 1);
-      if (i < s.n[0]) load(pages[0], i, 0);
+      }
     }
-    return ok;
+    return ld.ok;
   });
-  drain(p, ring, bars, ok);
+  ld.drain();
 }
 
-// One guard warp's share of a value tile (tokens from t0 on): rows that no
-// query row sees are cleared, non-finite elements of rows that some see are
-// taken out and their first token noted.
+// The guard warp on a value tile (tokens from t0 on) of segment k: rows that
+// no query row sees are cleared, non-finite elements of rows that some see
+// are taken out and their first token noted for this segment.  per_segment:
+// softmax warps that end each segment.
 template <typename T>
-__device__ void guard_tile(uint8_t *tile, int t0, int all, int none, int g, int *bad, volatile int *nonfinite) {
+__device__ __forceinline__ void guard_tile(const Attend16 &p, uint8_t *tile, int t0, int all, int none, int k,
+                                           int per_segment, int *bad, Flags *flags) {
   const uint32_t mask = exponent_mask<T>();
-  for (int r = max(0, all - t0) + (g >> 4); r < kTile; r += 4) {
-    const int chunk = g & 15;  // 16-byte chunk: half chunk / 8, swizzled by the row
-    uint4 *at = reinterpret_cast<uint4 *>(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (chunk & 7) * 16);
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int r) {  // this lane's 16 bytes of row r
+    const int c = lane & 15;
+    return reinterpret_cast<uint4 *>(tile + (c >> 3) * (kTileBytes / 2) + r * 128 + (c & 7) * 16);
+  };
+  bool any = false;
+#pragma unroll 4
+  for (int r = max(0, all - t0) + (lane >> 4); r < kTile; r += 2) {
     if (t0 + r >= none) {
-      *at = make_uint4(0u, 0u, 0u, 0u);
-      continue;
-    }
-    uint4 v = *at;
-    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-    bool any = false;
+      *at(r) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uint4 v = *at(r);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
-    if (any) {
-      const int dim0 = (chunk >> 3) * 64 + (((chunk & 7) ^ (r & 7)) * 8);
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu, m = mask & 0xffffu;
-        if ((x & m) != m) continue;
-        const int kind = (x & 0x7fffu) != m ? 2 : (x >> 15);
-        atomicMin(&bad[kind * kD + dim0 + e], t0 + r);
-        w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-      }
-      *nonfinite = 1;
-      *at = v;
+      for (int i = 0; i < 4; ++i)
+        any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
     }
   }
+  if (!__any_sync(0xffffffffu, any)) return;
+  // rare: an earlier segment's marks must have been read before they go
+  volatile int *marked = &flags->nonfinite, *done = &flags->done, *abort = &flags->abort;
+  const int before = *marked;
+  if (before != k + 1) {
+    const uint64_t start = global_ns();
+    while (*done < before * per_segment && !*abort && global_ns() - start < kWaitLimitNs) __nanosleep(200);
+    if (*done < before * per_segment) set_status(p.status, ISOQUANT_DEVERR_WAIT_TIMEOUT);
+    for (int e = lane; e < 3 * kD; e += 32) bad[e] = INT_MAX;
+    __syncwarp();
+  }
+  for (int r = max(0, all - t0) + (lane >> 4); r < min(kTile, none - t0); r += 2) {
+    uint4 v = *at(r);
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+    // the chunk lies where the row's swizzle put it
+    const int dim0 = ((lane & 15) >> 3) * 64 + (((lane & 7) ^ (r & 7)) * 8);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu, m = mask & 0xffffu;
+      if ((x & m) != m) continue;
+      const int kind = (x & 0x7fffu) != m ? 2 : (x >> 15);
+      atomicMin(&bad[kind * kD + dim0 + e], t0 + r);
+      w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+    }
+    *at(r) = v;
+  }
+  __syncwarp();
+  if (lane == 0) *marked = k + 1;
 }
 
-// The guard warps over the cache.
+// A loaded tile: seen to, then handed on.  phases: bit i = parity of slot i's loads.
 template <typename T>
-__device__ void guard_cache(const Attend16 &p, const int64_t *loc, uint8_t *ring_base, int *bad, Bars &bars,
-                            Flags *flags) {
-  const int lane = threadIdx.x & 31, g = threadIdx.x - kGuardWarp * 32;
-  volatile int *abort = &flags->abort, *nonfinite = &flags->nonfinite;
-  Ring ring(p.slots);
-  uint32_t n_clear = 0, n_go = 0;
-  bool ok = true;
+__device__ __forceinline__ bool guard_slot(const Attend16 &p, uint32_t sl, uint32_t &phases, uint8_t *ring_base, int t0,
+                                           int all, int none, int k, int per_segment, int *bad, Bars &bars,
+                                           Flags *flags) {
+  const bool ok = warp_wait(&bars.loaded[sl], (phases >> sl) & 1u, p, &flags->abort);
+  phases ^= 1u << sl;
+  if (!ok) return false;
+  guard_tile<T>(p, ring_base + sl * kTileBytes, t0, all, none, k, per_segment, bad, flags);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.full[sl]);
+  return true;
+}
+
+// The guard warp over the cache.
+template <typename T>
+__device__ void guard_cache(const Attend16 &p, const int64_t *loc, uint8_t *ring_base, int per_segment, int *bad,
+                            Bars &bars, Flags *flags) {
+  uint32_t phases = 0, t = 0;
   cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
     const int all = all_see(p, s), none = none_sees(p, s, p.tok), n = s.n[0];
-    bool fresh = k > 0;
-    for (int i = 0; i < n + 2; ++i) {
-      if (i >= 2 && i - 2 < n) {
-        const uint32_t rd = ring.round, sl = ring.step();
-        const int t0 = (s.j0 + i - 2) * kTile;
-        if (t0 + kTile > all && ok) {
-          // The MMA warp has the tile: the phases that the waits below name
-          // are those of this tile and of the segment before.
-          ok = warp_wait(&bars.go, n_go & 1u, p, abort);
-          ++n_go;
-          if (fresh) {
-            // the marks of the segment before are read no more
-            ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
-            fresh = false;
-            if (threadIdx.x < (kGuardWarp + 1) * 32) {
-              if (*nonfinite) {
-                for (int e = lane; e < 3 * kD; e += 32) bad[e] = INT_MAX;
-                __syncwarp();
-                if (lane == 0) *nonfinite = 0;
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.cleared);
-            } else {
-              ok = ok && warp_wait(&bars.cleared, n_clear & 1u, p, abort);
-            }
-            ++n_clear;
-          }
-          ok = ok && warp_wait(&bars.full[sl], rd & 1u, p, abort);
-          guard_tile<T>(ring_base + sl * kTileBytes, t0, all, none, g, bad, nonfinite);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&bars.guarded);
-        }
-      }
-      if (i < n) ring.step();
-    }
+    bool ok = true;
+    for (int i = max(0, all / kTile - s.j0); i < n && ok; ++i)
+      ok = guard_slot<T>(p, value_slot(t + i, p.slots), phases, ring_base, (s.j0 + i) * kTile, all, none, k, per_segment,
+                         bad, bars, flags);
+    t += n;
     return ok;
   });
 }
@@ -699,11 +738,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
   float2 *ml = reinterpret_cast<float2 *>(tail + kOffMl);
   Bars &bars = *reinterpret_cast<Bars *>(tail + kOffBar);
   Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
-  volatile int *abort = &flags->abort, *issued = &flags->issued, *nonfinite = &flags->nonfinite;
+  volatile int *abort = &flags->abort, *nonfinite = &flags->nonfinite;
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
   const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
 
-  start_cta<512>(bars, flags, bad, row_warps, row_warps);
+  start_cta<512>(bars, flags, bad, 2, 2, row_warps, row_warps);
   pdl_trigger();
   pdl_wait();
   Segment prompt{};
@@ -723,108 +762,102 @@ __global__ void __launch_bounds__(kThreads16, 1)
 
   // registers of the four helper warps go to the softmax threads:
   // 256 x 208 + 128 x 80 of the 384 x 168 at launch
-  if (warp == kMmaWarp) {
+  if (warp < 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // ------------------------------------------------------------------ MMA
-    const bool leader = lane == 0;
-    Ring ring(p.slots);
-    uint32_t n_p[2] = {0, 0}, n_guard = 0;
+    // ------------------------------------------------------------- products
+    // Each side has a warp that issues its products: issuing takes as long as
+    // the tensor cores need, so one warp's waits and commits would be time
+    // that they idle (one issuing warp for both: 490 us for a prompt of 8192
+    // tokens, 32 and 8 heads).
+    const int x = warp;
+    const uint32_t issue = lane == 0;
+    uint32_t n_p = 0, t = 0, n_turn = 0;  // weights, tiles, turns so far
     bool ok = true;
-    auto take = [&]() {  // waits for the next slot's tile
-      ok = ok && warp_wait(&bars.full[ring.slot], ring.round & 1u, p, abort);
-      return ring.step();
+    auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity, p, abort); };
+    // Both warps go through all tiles: what only the other side uses is passed,
+    // so that each sees every phase of a slot.
+    auto keys = [&](uint32_t tile) {
+      wait(&bars.full[key_slot(tile)], key_use(tile) & 1u);
+      return key_slot(tile);
     };
-    const uint64_t dK = desc128(smem_addr(ring_base), 1, 64),
-                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64);
-    const uint32_t q_units = static_cast<uint32_t>(p.q_half) >> 4;
-    auto issue_s = [&](int x, int qb, uint32_t sl) {
-      tc_fence_after();
-      if (leader && ok) {
-        *issued = 1;
-        const uint64_t a = desc128(smem_addr(smem), 1, 64) + static_cast<uint64_t>(qb) * 2 * q_units;
-        const uint64_t b = dK + sl * (kTileBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + 128 * x, a + (k >> 2) * static_cast<uint64_t>(q_units) + 2 * (k & 3),
-                 b + (k >> 2) * (kTileBytes >> 5) + 2 * (k & 3), idesc16<T>(kTile, 0, 0), k > 0);
-        umma_commit(&bars.s_full[x]);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int x, uint32_t sl, bool first, bool guard) {
-      if (guard && ok && leader) mbar_arrive(&bars.go);
-      __syncwarp();
-      ok = ok && warp_wait(&bars.p_full[x], n_p[x] & 1u, p, abort);
-      ++n_p[x];
-      if (guard) {
-        ok = ok && warp_wait(&bars.guarded, n_guard & 1u, p, abort);
-        ++n_guard;
-      }
-      tc_fence_after();
-      if (leader && ok) {
-        const uint64_t b = dV + sl * (kTileBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, b + 128 * k, idesc16<T>(kTile, 0, 1), !first || k > 0);
-        if constexpr (kLo) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * k, b + 128 * k, idesc16<T>(kTile, 0, 1), 1);
-        }
-      }
-      __syncwarp();
+    auto values = [&](uint32_t tile) {
+      const uint32_t sl = value_slot(tile, kRowSlots);
+      wait(&bars.full[sl], value_use(tile, kRowSlots) & 1u);
+      return sl;
     };
     auto commit = [&](uint64_t *bar) {
-      if (leader && ok) umma_commit(bar);
-      __syncwarp();
+      if (ok) umma_commit_by(issue, bar);
+    };
+    auto arrive = [&](uint64_t *bar) {
+      if (ok && issue) mbar_arrive(bar);
+    };
+    const uint64_t dK = desc128(smem_addr(ring_base), 1, 64),
+                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64), dQ = desc128(smem_addr(smem), 1, 64);
+    auto issue_s = [&](int qb, uint32_t sl) {
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t a = dQ + static_cast<uint64_t>(qb) * (kTileBytes >> 4), b = dK + sl * (kTileBytes >> 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        mma_ss(issue, tmem + 128 * x, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
+               b + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3), idesc16<T>(kTile, 0, 0), q > 0);
+      umma_commit_by(issue, &bars.s_full[x]);
+    };
+    auto issue_pv = [&](uint32_t sl, bool first) {
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t b = dV + sl * (kTileBytes >> 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, b + 128 * q, idesc16<T>(kTile, 0, 1),
+               !first || q > 0);
+      if constexpr (kLo) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * q, b + 128 * q, idesc16<T>(kTile, 0, 1), 1);
+      }
     };
     for_segments([&](const Segment &s, uint32_t k) {
-      const int all = all_see(p, s);
-      if constexpr (kPaged) {
-        const int n = s.n[0], qb = k & 1;
-        ok = ok && warp_wait(&bars.q_full[qb], (k >> 1) & 1u, p, abort);
-        for (int i = 0; i < n + 2 && ok; ++i) {
-          const int x = i & 1;
-          if (i >= 2 && i - 2 < n) {
-            const uint32_t sl = take();
-            issue_pv(x, sl, i - 2 < 2, (s.j0 + i - 1) * kTile > all);
-            commit(&bars.freed[sl]);
-            if (i >= n) commit(&bars.o_done[x]);
-          }
-          if (i < n) {
-            const uint32_t sl = take();
-            issue_s(x, qb, sl);
-            commit(&bars.freed[sl]);
-            if (i == n - 1) commit(&bars.q_free[qb]);
-          }
-        }
-      } else {
-        const int n = max(s.n[0], s.n[1]);
+      const int qb = kPaged ? k & 1 : x, n = kPaged ? s.n[0] : max(s.n[0], s.n[1]);
+      if (kPaged || s.n[x] > 0) wait(&bars.q_full[qb], kPaged ? (k >> 1) & 1u : 0u);
+      if (kPaged && x >= n) arrive(&bars.q_free[qb]);
+      // prompts: this side's tiles are the first s.n[x]; cache: each second
+      const int first = kPaged ? x : 0, step = kPaged ? 2 : 1, last = kPaged ? n : s.n[x];
+      auto mine = [&](int i) { return i < last && (!kPaged || (i & 1) == x); };
+      for (int i = 0; i < n + step && ok; ++i) {
+        // the product of tile i - step, then the scores of tile i: both tiles first
+        const bool has_v = i >= step;
         uint32_t v_slot = 0, k_slot = 0;
-        for (int j = 0; j <= n && ok; ++j) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // the first side to need a tile waits for it, the last frees it
-            const int other = s.n[1 - x];
-            if (j > 0 && j - 1 < s.n[x]) {
-              const bool first_user = x == 0 || j - 1 >= other;
-              if (first_user) v_slot = take();
-              issue_pv(x, v_slot, j == 1, first_user && j * kTile > all);
-              if (x == 1 || j - 1 >= other) commit(&bars.freed[v_slot]);
-              if (j == s.n[x]) commit(&bars.o_done[x]);
-            }
-            if (j < s.n[x]) {
-              if (j == 0) ok = ok && warp_wait(&bars.q_full[x], 0, p, abort);
-              if (x == 0 || j >= other) k_slot = take();
-              issue_s(x, x, k_slot);
-              if (x == 1 || j >= other) commit(&bars.freed[k_slot]);
-            }
+        if (has_v) v_slot = values(t + i - step);
+        if (i < n) k_slot = keys(t + i);
+        if (has_v && mine(i - step)) wait(&bars.p_full[x], n_p++ & 1u);
+        // the sides take turns
+        if (x == 1 || n_turn > 0) wait(&bars.turn[x], (n_turn - (x == 0)) & 1u);
+        ++n_turn;
+        if (has_v) {
+          if (mine(i - step)) {
+            issue_pv(v_slot, i - step == first);
+            commit(&bars.freed[v_slot]);
+            if (i >= last) commit(&bars.o_done[x]);
+          } else {
+            arrive(&bars.freed[v_slot]);
           }
         }
+        if (i < n) {
+          if (mine(i)) {
+            issue_s(qb, k_slot);
+            commit(&bars.freed[k_slot]);
+            if (kPaged && i + 2 >= n) commit(&bars.q_free[qb]);
+          } else {
+            arrive(&bars.freed[k_slot]);
+          }
+        }
+        arrive(&bars.turn[1 - x]);
       }
+      t += n;
       return ok;
     });
-    if (*issued) umma_commit_by(leader, &bars.mma_done);
+    umma_commit_by(issue, &bars.mma_done);
   } else if (warp == kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if constexpr (kPaged) {
@@ -832,8 +865,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
     } else if (has_prompt) {
       const Segment &s = prompt;
       const uint32_t sq = smem_addr(smem), sr = smem_addr(ring_base);
-      Ring ring(p.slots);
-      bool ok = true;
+      Loader ld(p, bars, abort);
       // box of a Q tile: 64 dims x G heads x tok tokens
       auto load_q = [&](int x) {
         if (s.n[x] && lane == 0) {
@@ -845,48 +877,34 @@ __global__ void __launch_bounds__(kThreads16, 1)
         __syncwarp();
       };
       load_q(0);
-      const int n = max(s.n[0], s.n[1]);
-      for (int j = 0; j < n && ok; ++j) {
+      const int n = max(s.n[0], s.n[1]), all = all_see(p, s);
+      for (int j = 0; j < n && ld.ok; ++j) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (ring.round > 0) ok = ok && warp_wait(&bars.freed[ring.slot], (ring.round - 1) & 1u, p, abort);
-          if (!ok) break;
-          const uint32_t sl = ring.step();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars.full[sl], kTileBytes);
+          const uint32_t sl = kv ? value_slot(j, kRowSlots) : key_slot(j);
+          uint64_t *bar = ld.begin(sl, kv ? value_use(j, kRowSlots) : key_use(j), kv && (j + 1) * kTile > all, kTileBytes);
+          if (lane == 0 && ld.ok) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-              tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile,
-                     &bars.full[sl]);
+              tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile, bar);
           }
           __syncwarp();
           if (j == 0 && kv == 0) load_q(1);
         }
       }
-      drain(p, ring, bars, ok);
+      ld.drain();
     }
-  } else if (warp < 4) {
+  } else if (warp == kGuardWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if constexpr (kPaged) {
-      guard_cache<T>(p, loc, ring_base, bad, bars, flags);
+      guard_cache<T>(p, loc, ring_base, row_warps, bad, bars, flags);
     } else if (has_prompt) {
       const Segment &s = prompt;
       const int all = all_see(p, s), none = none_sees(p, s, 2 * p.tok), n = max(s.n[0], s.n[1]);
-      Ring ring(p.slots);
-      uint32_t n_go = 0;
+      uint32_t phases = 0;
       bool ok = true;
-      for (int j = 0; j < n && ok; ++j) {
-        ring.step();
-        const uint32_t rd = ring.round, sl = ring.step();
-        if ((j + 1) * kTile <= all) continue;
-        ok = warp_wait(&bars.go, n_go & 1u, p, abort) && warp_wait(&bars.full[sl], rd & 1u, p, abort);
-        ++n_go;
-        if (!ok) break;
-        guard_tile<T>(ring_base + sl * kTileBytes, j * kTile, all, none, tid - kGuardWarp * 32, bad, nonfinite);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.guarded);
-      }
+      for (int j = all / kTile; j < n && ok; ++j)
+        ok = guard_slot<T>(p, value_slot(j, kRowSlots), phases, ring_base, j * kTile, all, none, 0, 0, bad, bars, flags);
     }
   } else {
     // -------------------------------------------------------------- softmax
@@ -898,10 +916,10 @@ __global__ void __launch_bounds__(kThreads16, 1)
     uint32_t n_s = 0, n_o1 = 0;
     bool ok = true;
     // one row's sum of products, times f, plus what the guards took out
-    auto finish = [&](int lim, float (&o)[32], int col, float f) {
+    auto finish = [&](uint32_t k, int lim, float (&o)[32], int col, float f) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= f;
-      if (*nonfinite) {
+      if (*nonfinite == static_cast<int>(k) + 1) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = with_nonfinite(o[i], bad, col + i, lim);
       }
@@ -949,7 +967,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
         for (int col = 0; col < kD; col += 32) {
           float o[32];
           tmem_ld32(to + col, o);
-          finish(lim, o, col, inv);
+          finish(k, lim, o, col, inv);
           if (valid) store16(dst + col, o);
         }
       } else if (x == 1) {
@@ -994,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
           }
-          finish(lim, o, col, s.whole ? inv : 1.f);
+          finish(k, lim, o, col, s.whole ? inv : 1.f);
           if (valid) {
             if (s.whole) {
               store16(dst + col, o);
@@ -1008,7 +1026,10 @@ __global__ void __launch_bounds__(kThreads16, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.seg_done);
+        if (lane == 0) {
+          mbar_arrive(&bars.seg_done);
+          atomicAdd(&flags->done, 1);
+        }
       }
       return true;
     });
@@ -1104,11 +1125,11 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
   int *bad = reinterpret_cast<int *>(tail + kOffBad);
   Bars &bars = *reinterpret_cast<Bars *>(tail + kOffBar);
   Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
-  volatile int *abort = &flags->abort, *issued = &flags->issued, *nonfinite = &flags->nonfinite;
+  volatile int *abort = &flags->abort, *nonfinite = &flags->nonfinite;
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
   const int soft_warps = (p.R + SR - 1) / SR * 4;  // sides without rows rest
 
-  start_cta<C::kCols>(bars, flags, bad, soft_warps, soft_warps);
+  start_cta<C::kCols>(bars, flags, bad, 1, 1, soft_warps, soft_warps);
   // Q rows that no copy writes are zero
   for (int i = tid; i < C::kP / 16; i += C::kThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1118,80 +1139,65 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = flags->tmem;
 
-  if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA
-    const bool leader = lane == 0;
-    Ring ring(C::kSlots);
-    uint32_t n_p = 0, n_s = 0, n_guard = 0;  // tiles, guarded tiles so far
+  if (warp < 2) {
+    // ------------------------------------------------------------- products
+    // warp 0 issues the scores, warp 1 the products with the values
+    const uint32_t issue = lane == 0;
+    uint32_t tiles = 0;
     bool ok = true;
-    auto take = [&]() {
-      ok = ok && warp_wait(&bars.full[ring.slot], ring.round & 1u, p, abort);
-      return ring.step();
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity, p, abort); };
     auto commit = [&](uint64_t *bar) {
-      if (leader && ok) umma_commit(bar);
-      __syncwarp();
+      if (ok) umma_commit_by(issue, bar);
     };
     const uint64_t dK = desc128(smem_addr(ring_base), 1, 64),
-                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64);
+                   dV = desc128(smem_addr(ring_base), kTileBytes / 32, 64), dQ = desc128(smem_addr(smem), 1, 64),
+                   dP = desc_plain(smem_addr(smem + C::kP), 8, 128);
     cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
-      const int all = all_see(p, s), n = s.n[0];
-      const uint32_t qb = k % C::kQBufs, use = k / C::kQBufs;
-      ok = ok && warp_wait(&bars.q_full[qb], use & 1u, p, abort);
-      for (int i = 0; i < n + 2 && ok; ++i) {
-        // The ring holds K0 K1 V0 K2 V1 ..: the scores of tile i go first, to
-        // the buffer that tile i - 2 left (its weights were waited for below).
-        const bool has_v = i >= 2 && i - 2 < n;
-        uint32_t v_slot = 0;
-        if (has_v) v_slot = take();
-        if (has_v) {
-          const bool guard = (s.j0 + i - 1) * kTile > all;
-          if (guard && leader && ok) mbar_arrive(&bars.go);
-          __syncwarp();
-          ok = ok && warp_wait(&bars.p_full[n_p & 1u], (n_p >> 1) & 1u, p, abort);
-          if (guard) {
-            ok = ok && warp_wait(&bars.guarded, n_guard & 1u, p, abort);
-            ++n_guard;
-          }
-          tc_fence_after();
-          if (leader && ok) {
-            const uint64_t a = dV + v_slot * (kTileBytes >> 4);
-            const uint64_t b = desc_plain(smem_addr(smem + C::kP + n_p % C::kPBufs * C::kPBytes), 8, 128);
+      const int n = s.n[0];
+      if (warp == 0) {
+        const uint32_t qb = k % C::kQBufs, use = k / C::kQBufs;
+        wait(&bars.q_full[qb], use & 1u);
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t sl = key_slot(tiles), buf = tiles & 1u;
+          wait(&bars.full[sl], key_use(tiles) & 1u);
+          if (tiles >= 2) wait(&bars.s_free[buf], ((tiles >> 1) + 1u) & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint64_t a = dK + sl * (kTileBytes >> 4), b = dQ + qb * (C::kQBytes >> 4);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              mma_ss(tmem + C::kColO, a + 128 * q, b + 16 * q, idesc16<T>(C::kN, 1, 1), i > 2 || q > 0);
-          }
-          __syncwarp();
-          commit(&bars.freed[v_slot]);
-          commit(&bars.o_done[n_p & 1u]);
-          ++n_p;
-        }
-        if (i < n) {
-          const uint32_t sl = take();
-          tc_fence_after();
-          if (leader && ok) {
-            *issued = 1;
-            const uint64_t a = dK + sl * (kTileBytes >> 4);
-            const uint64_t b = desc128(smem_addr(smem) + qb * C::kQBytes, 1, 64);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              mma_ss(tmem + (n_s & 1u) * NR, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
+              mma_ss(issue, tmem + buf * NR, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
                      b + (q >> 2) * (C::kQBytes >> 5) + 2 * (q & 3), idesc16<T>(NR, 0, 0), q > 0);
-            umma_commit(&bars.s_full[n_s & 1u]);
           }
-          __syncwarp();
-          ++n_s;
+          commit(&bars.s_full[buf]);
           commit(&bars.freed[sl]);
           if (i == n - 1) commit(&bars.q_free[qb]);
+          ++tiles;
+        }
+      } else {
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t sl = value_slot(tiles, C::kSlots), buf = tiles & 1u;
+          wait(&bars.full[sl], value_use(tiles, C::kSlots) & 1u);
+          wait(&bars.p_full[buf], (tiles >> 1) & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint64_t a = dV + sl * (kTileBytes >> 4), b = dP + tiles % C::kPBufs * (C::kPBytes >> 4);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mma_ss(issue, tmem + C::kColO, a + 128 * q, b + 16 * q, idesc16<T>(C::kN, 1, 1), i > 0 || q > 0);
+          }
+          commit(&bars.freed[sl]);
+          commit(&bars.o_done[buf]);
+          ++tiles;
         }
       }
       return ok;
     });
-    if (*issued) umma_commit_by(leader, &bars.mma_done);
+    umma_commit_by(issue, &bars.mma_done);
   } else if (warp == kLoadWarp) {
     load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), C::kQBufs, bars, abort);
-  } else if (warp < 4) {
-    guard_cache<T>(p, loc, ring_base, bad, bars, flags);
+  } else if (warp == kGuardWarp) {
+    guard_cache<T>(p, loc, ring_base, soft_warps, bad, bars, flags);
   } else {
     // -------------------------------------------------------------- softmax
     const int x = (warp >> 2) - 1, t = tid & (kTile - 1), row0 = x * SR;
@@ -1205,14 +1211,13 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
     const int tok0 = row0 / p.GB, head0 = row0 - tok0 * p.GB;
     uint32_t n_s = 0;  // tiles so far
     bool ok = true;
-    // Waits for the product of tile n_s - 1.  The tiles take the two barriers
-    // in turn: that of tile n_s - 3 is done (tile n_s - 1's scores came after
-    // it), so the parity names one phase.
-    auto last_product = [&]() {
-      return warp_wait(&bars.o_done[(n_s - 1) & 1u], ((n_s - 1) >> 1) & 1u, p, abort);
-    };
+    // Waits for the product of an earlier tile.  The tiles take the two barriers
+    // in turn; that of two tiles before was waited for already (a tile's
+    // weights wait below for the last reader of their buffer, or a later one),
+    // so the parity names one phase.
+    auto product = [&](uint32_t tile) { return warp_wait(&bars.o_done[tile & 1u], (tile >> 1) & 1u, p, abort); };
     // Every warp of a side goes through the same barriers, after a failed wait too.
-    if (warp < 4 + soft_warps) cache_segments(p, loc, [&](const Segment &s, uint32_t) {
+    if (warp < 4 + soft_warps) cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
       const int all = all_see(p, s), n = s.n[0];
       float2 l[SR / 2];
 #pragma unroll
@@ -1223,6 +1228,9 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
         tc_fence_after();
         float v[SR];
         tmem_ld_cols<SR>(ts + (n_s & 1u) * NR, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&bars.s_free[n_s & 1u]);
         if ((s.j0 + i + 1) * kTile > all) {
           int qi = s.row0 + tok0, head = head0, lim = s.limit(qi, p.causal);
 #pragma unroll
@@ -1266,7 +1274,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
           side_sync(x);
           if (i > 0) {
             // the last product must be done
-            ok = ok && last_product();
+            ok = ok && product(n_s - 1);
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < SR; r += 2)
@@ -1298,9 +1306,8 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
               e[at] = pack16(pr.x - __uint_as_float(w[at] << 16), pr.y - __uint_as_float(w[at] & 0xffff0000u), T());
           }
         }
-        // the buffer of P: with one, the last product must have read it; with
-        // two, these scores came behind the product that read it
-        if (C::kPBufs == 1 && n_s > 0) ok = ok && last_product();
+        // the last product that read this buffer of P
+        if (n_s >= C::kPBufs) ok = ok && product(n_s - C::kPBufs);
         uint8_t *dst = smem + C::kP + n_s % C::kPBufs * C::kPBytes + (row0 >> 3) * (kTile * 16) + t * 16;
 #pragma unroll
         for (int g = 0; g < SR / 8; ++g) {
@@ -1333,7 +1340,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
           *reinterpret_cast<float2 *>(rec + 2 * (row0 + t)) =
               make_float2(refs[t] - kShift<T>, sum);
       }
-      ok = ok && last_product();
+      ok = ok && product(n_s - 1);
       tc_fence_after();
       side_sync(x);
       // thread t: dim t of the side's rows
@@ -1353,7 +1360,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
         for (int r = 0; r < SR; ++r) {
           if (row0 + r < p.R && qi < s.rows && head < heads) {
             float y = o[r] * factor[r];
-            if (*nonfinite) y = with_nonfinite(y, bad, t, s.limit(qi, p.causal));
+            if (*nonfinite == static_cast<int>(k) + 1) y = with_nonfinite(y, bad, t, s.limit(qi, p.causal));
             if (s.whole) out[((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq + head) * kD] = to16(y, T());
             else rec[2 * p.row_stride + (row0 + r) * kD + t] = y;
           }
@@ -1365,7 +1372,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
       }
       tc_fence_before();
       side_sync(x);  // sums and factors are read
-      if (lane == 0 && ok) mbar_arrive(&bars.seg_done);
+      if (lane == 0) atomicAdd(&flags->done, 1);
       return true;
     });
   }
@@ -1488,7 +1495,7 @@ cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &m
   if (p.R <= 16) return launch_cols<T, 16>(p, mq, mk, grid, stream);
   if (p.R <= 32) return launch_cols<T, 32>(p, mq, mk, grid, stream);
   if (p.R <= 64) return launch_cols<T, 64>(p, mq, mk, grid, stream);
-  p.slots = 5;
+  p.slots = kRowSlots;
   p.q_half = kTileBytes / 2;
   return launch_tiles(k_attend16<T, true>, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
 }
@@ -1519,7 +1526,7 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   p.c = scale * 1.4426950408889634f;
   p.cu = cu_seqlens;
   p.n_tok = n_tok;
-  p.slots = 5;
+  p.slots = kRowSlots;
   p.q_half = kTileBytes / 2;
   p.out = out;
   p.status = ctx->status;
