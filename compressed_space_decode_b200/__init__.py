@@ -131,8 +131,8 @@ def _check(status, what):
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current device's current stream (without building a Stream object)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -301,25 +301,35 @@ def isoquant_decode_prep(ctx, cache, k, v, slot_mapping, q, q_rot, stream=None):
            "isoquant_decode_prep")
 
 
+# The checks of the calls below are tuple comparisons on attributes read once:
+# a decode step's kernels take a few microseconds, which the host has to keep
+# up with.
+
+def _address(t):
+    return t.data_ptr() if t is not None else None
+
+
 def _positions(t, n):
-    assert t.dtype == torch.int64 and t.is_contiguous() and t.numel() == n
+    assert t.dtype is torch.int64 and t.shape == (n,) and t.is_contiguous()
 
 
 def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_rot, stream=None):
     """isoquant_decode_prep with keys rotated to positions k_pos (int64
     [n_tok]) before they are compressed and query rows to q_pos (int64
     [n_rows]) before R; rope: Rope."""
-    assert k.is_contiguous() and v.is_contiguous() and k.shape == v.shape
-    assert q.is_contiguous() and q_rot.is_contiguous() and q_rot.dtype == torch.float32 and q_rot.shape == q.shape
-    assert k.dtype == v.dtype == q.dtype
-    _positions(slot_mapping, k.shape[0])
-    _positions(k_pos, k.shape[0])
-    _positions(q_pos, q.shape[0])
-    cs = cache.c_struct()
-    _check(lib().isoquant_decode_prep_rope(ctx.handle, cs, _ptr(k), _ptr(v), k.shape[0], _ptr(slot_mapping),
-                                           _ptr(k_pos), _ptr(q), _dtype(q), q.shape[0], q.shape[1], _ptr(q_pos),
-                                           rope.c_struct(), _ptr(q_rot), _stream(stream)),
-           "isoquant_decode_prep_rope")
+    n, rows = k.shape[0], q.shape[0]
+    assert k.shape == v.shape == (n, ctx.num_kv_heads, HEAD_DIM) and k.is_contiguous() and v.is_contiguous()
+    assert q.shape == q_rot.shape == (rows, q.shape[1], HEAD_DIM) and q.is_contiguous() and q_rot.is_contiguous()
+    assert k.dtype is v.dtype is q.dtype and q_rot.dtype is torch.float32
+    _positions(slot_mapping, n)
+    _positions(k_pos, n)
+    _positions(q_pos, rows)
+    status = lib().isoquant_decode_prep_rope(ctx.handle, cache.c_struct(), k.data_ptr(), v.data_ptr(), n,
+                                             slot_mapping.data_ptr(), k_pos.data_ptr(), q.data_ptr(), _dtype(q), rows,
+                                             q.shape[1], q_pos.data_ptr(), rope.c_struct(), q_rot.data_ptr(),
+                                             _stream(stream))
+    if status:
+        _check(status, "isoquant_decode_prep_rope")
 
 
 def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_out, k_out=None, stream=None):
@@ -329,23 +339,25 @@ def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q
     receives the rotated keys of every token.  rope None: no rotation (the
     positions may be None).  cache None: only k_out and q_out are written (v
     and slot_mapping may be None)."""
-    assert k.is_contiguous() and q.is_contiguous() and q_out.is_contiguous()
-    assert k.dtype == q.dtype == q_out.dtype and q_out.shape == q.shape
-    assert k.dim() == 3 and k.shape[1] == ctx.num_kv_heads and k.shape[2] == HEAD_DIM
-    assert q.dim() == 3 and q.shape[2] == HEAD_DIM
+    n, rows, dtype = k.shape[0], q.shape[0], k.dtype
+    assert k.shape == (n, ctx.num_kv_heads, HEAD_DIM) and k.is_contiguous()
+    assert q.shape == q_out.shape == (rows, q.shape[1], HEAD_DIM) and q.is_contiguous() and q_out.is_contiguous()
+    assert q.dtype is dtype and q_out.dtype is dtype
     if cache is not None:
-        assert v.is_contiguous() and v.shape == k.shape and v.dtype == k.dtype
+        assert v.shape == k.shape and v.is_contiguous() and v.dtype is dtype
         assert cache.num_kv_heads == ctx.num_kv_heads
-        _positions(slot_mapping, k.shape[0])
+        _positions(slot_mapping, n)
     if rope is not None:
-        _positions(k_pos, k.shape[0])
-        _positions(q_pos, q.shape[0])
+        _positions(k_pos, n)
+        _positions(q_pos, rows)
     if k_out is not None:
-        assert k_out.is_contiguous() and k_out.shape == k.shape and k_out.dtype == k.dtype
-    _check(lib().isoquant_dense_prep(ctx.handle, cache.c_struct() if cache is not None else None, _ptr(k), _ptr(v),
-                                     k.shape[0], _ptr(slot_mapping), _ptr(k_pos), _ptr(q), _dtype(q), q.shape[0],
-                                     q.shape[1], _ptr(q_pos), rope.c_struct() if rope is not None else None,
-                                     _ptr(k_out), _ptr(q_out), _stream(stream)), "isoquant_dense_prep")
+        assert k_out.shape == k.shape and k_out.is_contiguous() and k_out.dtype is dtype
+    status = lib().isoquant_dense_prep(ctx.handle, cache.c_struct() if cache is not None else None, k.data_ptr(),
+                                       _address(v), n, _address(slot_mapping), _address(k_pos), q.data_ptr(), _dtype(q),
+                                       rows, q.shape[1], _address(q_pos), rope.c_struct() if rope is not None else None,
+                                       _address(k_out), q_out.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "isoquant_dense_prep")
 
 
 def isoquant_dense_workspace_size(ctx, batch, nq, num_q_heads):
@@ -364,16 +376,18 @@ def isoquant_dense_attend(ctx, cache, q, page_table, seq_lens, workspace, out, c
     """Attention of the newest tokens over a DenseCache: q and out
     [B][nq][Hq][128] of the cache's dtype; page_table int32 [B][max_pages];
     seq_lens int32 [B]; workspace from alloc_dense_workspace."""
-    assert q.is_contiguous() and q.dim() == 4 and q.shape[3] == HEAD_DIM and q.dtype == cache.data.dtype
-    assert out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
-    assert page_table.dtype == torch.int32 and page_table.is_contiguous() and page_table.shape[0] == q.shape[0]
-    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() == q.shape[0]
+    B, nq, Hq, D = q.shape
+    dtype, max_pages = cache.data.dtype, page_table.shape[1]
+    assert D == HEAD_DIM and q.dtype is dtype and q.is_contiguous()
+    assert out.shape == q.shape and out.dtype is dtype and out.is_contiguous()
+    assert page_table.shape == (B, max_pages) and page_table.dtype is torch.int32 and page_table.is_contiguous()
+    assert seq_lens.shape == (B,) and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()
     assert cache.num_kv_heads == ctx.num_kv_heads
-    B, nq, Hq, _ = q.shape
-    _check(lib().isoquant_dense_attend(ctx.handle, cache.c_struct(), _ptr(q), B, nq, Hq, _ptr(page_table),
-                                       page_table.shape[1], _ptr(seq_lens), int(bool(causal)), float(scale),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
-                                       _stream(stream)), "isoquant_dense_attend")
+    status = lib().isoquant_dense_attend(ctx.handle, cache.c_struct(), q.data_ptr(), B, nq, Hq, page_table.data_ptr(),
+                                         max_pages, seq_lens.data_ptr(), 1 if causal else 0, scale,
+                                         workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "isoquant_dense_attend")
 
 
 def isoquant_prompt_attend(ctx, q, k, v, cu_seqlens, out, causal=True, scale=0.0, stream=None):
@@ -381,19 +395,23 @@ def isoquant_prompt_attend(ctx, q, k, v, cu_seqlens, out, causal=True, scale=0.0
     [T][H][128] (bf16 or fp16; q, k and v may be slices of one projection:
     tokens any multiple of 8 elements apart, heads contiguous); cu_seqlens
     int32 [batch + 1]."""
-    for t in (q, k, v):
-        assert t.dim() == 3 and t.shape[2] == HEAD_DIM and t.stride(2) == 1
-        assert t.shape[1] == 1 or t.stride(1) == HEAD_DIM
-    assert k.shape[1] == v.shape[1] == ctx.num_kv_heads and q.shape[0] == k.shape[0] == v.shape[0]
-    assert q.dtype == k.dtype == v.dtype == out.dtype
-    assert out.is_contiguous() and out.shape == q.shape
-    assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 1
-    T, Hq, _ = q.shape
-    # a single token's stride is arbitrary
-    qs, ks, vs = ((t.stride(0) if T > 1 else t.shape[1] * HEAD_DIM) for t in (q, k, v))
-    _check(lib().isoquant_prompt_attend(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _dtype(q), T, Hq, qs, ks, vs,
-                                        _ptr(cu_seqlens), cu_seqlens.numel() - 1, int(bool(causal)), float(scale),
-                                        _ptr(out), _stream(stream)), "isoquant_prompt_attend")
+    T, Hq, D = q.shape
+    H, dtype = ctx.num_kv_heads, q.dtype
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    assert D == HEAD_DIM and k.shape == v.shape == (T, H, HEAD_DIM)
+    assert qs[2] == ks[2] == vs[2] == 1
+    # (the stride of a single head is arbitrary)
+    assert (Hq == 1 or qs[1] == HEAD_DIM) and (H == 1 or ks[1] == vs[1] == HEAD_DIM)
+    assert k.dtype is dtype and v.dtype is dtype and out.dtype is dtype
+    assert out.shape == q.shape and out.is_contiguous()
+    assert cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
+    if T <= 1:  # as is that of a single token
+        qs, ks, vs = (Hq * HEAD_DIM,), (H * HEAD_DIM,), (H * HEAD_DIM,)
+    status = lib().isoquant_prompt_attend(ctx.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), T, Hq,
+                                          qs[0], ks[0], vs[0], cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
+                                          1 if causal else 0, scale, out.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "isoquant_prompt_attend")
 
 
 def isoquant_step_workspace_size(ctx, batch, nq, num_q_heads):

@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -72,6 +73,7 @@ struct Attend16 {
   int slots, q_half;                                // ring slots, bytes of a 64-dim half of a Q buffer
   void *out;
   uint32_t *status;
+  int device;
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -1474,12 +1476,17 @@ void row_tiles(Attend16 &p, int group) {
   p.tok = kTile / p.GB;
 }
 
-// a kernel's launch with its dynamic shared memory
-template <typename... P, typename... A>
-cudaError_t launch_tiles(void (*kernel)(P...), int threads, int smem, unsigned grid, cudaStream_t stream,
-                         const A &...args) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
+// A kernel's launch with its dynamic shared memory, allowed once per device.
+template <auto kernel, typename... A>
+cudaError_t launch_tiles(int device, int threads, int smem, unsigned grid, cudaStream_t stream, const A &...args) {
+  static std::atomic<uint64_t> allowed{0};
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (device >= 64 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
 }
 int rows_smem(const Attend16 &p) { return 4 * p.q_half + p.slots * kTileBytes + kOffMl + kTile * 8; }
 
@@ -1487,7 +1494,7 @@ template <typename T, int NR>
 cudaError_t launch_cols(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid, cudaStream_t stream) {
   p.slots = Cols<T, NR>::kSlots;
   p.q_half = Cols<T, NR>::kQBytes / 2;
-  return launch_tiles(k_cols16<T, NR>, Cols<T, NR>::kThreads, Cols<T, NR>::kBytes, grid, stream, p, mq, mk);
+  return launch_tiles<k_cols16<T, NR>>(p.device, Cols<T, NR>::kThreads, Cols<T, NR>::kBytes, grid, stream, p, mq, mk);
 }
 template <typename T>
 cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &mk, unsigned grid,
@@ -1497,7 +1504,7 @@ cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &m
   if (p.R <= 64) return launch_cols<T, 64>(p, mq, mk, grid, stream);
   p.slots = kRowSlots;
   p.q_half = kTileBytes / 2;
-  return launch_tiles(k_attend16<T, true>, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
+  return launch_tiles<k_attend16<T, true>>(p.device, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
 }
 
 // the cache's row tiles: rows, and the stride of a record's rows
@@ -1530,6 +1537,7 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   p.q_half = kTileBytes / 2;
   p.out = out;
   p.status = ctx->status;
+  p.device = ctx->device;
   CUtensorMap mq, mk, mv;
   if (!encode_rows(&mq, dtype, q, n_tok, p.Hq, q_stride, p.GB, p.tok) ||
       !encode_rows(&mk, dtype, k, n_tok, p.H, k_stride, 1, kTile) ||
@@ -1540,8 +1548,8 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(grid);
   return dtype == ISOQUANT_BF16
-             ? launch_tiles(k_attend16<__nv_bfloat16, false>, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv)
-             : launch_tiles(k_attend16<__half, false>, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv);
+             ? launch_tiles<k_attend16<__nv_bfloat16, false>>(p.device, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv)
+             : launch_tiles<k_attend16<__half, false>>(p.device, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv);
 }
 
 size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s) {
@@ -1572,6 +1580,7 @@ cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_ca
   p.records = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(p.n_cta));
   p.out = out;
   p.status = ctx->status;
+  p.device = ctx->device;
   CUtensorMap mq, mk;
   const int64_t rows = static_cast<int64_t>(cache->num_pages) * 2 * p.H * cache->page_size;
   const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
