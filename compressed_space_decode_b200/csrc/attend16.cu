@@ -56,7 +56,7 @@ constexpr int kThreads16 = 3 * 128;         // k_attend16: two sides
 constexpr int kOffBad = 0;                      // first token with +inf, -inf, NaN of each dim
 constexpr int kOffBar = kOffBad + 3 * kD * 4;   // barriers
 constexpr int kOffFlags = kOffBar + 320;
-constexpr int kOffLoc = kOffFlags + 16;         // the CTA's part, then locate's scratch
+constexpr int kOffLoc = kOffFlags + 16;         // cache: the CTA's part, then locate's scratch; prompts: two jobs
 constexpr int kTailBytes = kOffLoc + 160;
 constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (reference, sum) of each row
 
@@ -148,6 +148,30 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
           dst),
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
+}
+// Asks the hardware for a CTA of this grid that has not started (it then never
+// will); the answer's 16 bytes complete on `bar`.  One thread.
+__device__ __forceinline__ void steal_request(uint4 *answer, uint64_t *bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_addr(answer)),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+// the answer: false if none was left, else the block's index
+__device__ __forceinline__ bool steal_answer(const uint4 *answer, uint32_t &block) {
+  const uint64_t lo = reinterpret_cast<const volatile uint64_t *>(answer)[0],
+                 hi = reinterpret_cast<const volatile uint64_t *>(answer)[1];
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n mov.b128 r, {%2, %3};\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "l"(lo), "l"(hi));
+  block = x;
+  return got != 0;
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
   asm volatile(
@@ -375,16 +399,16 @@ struct Walk16 {
   }
 };
 
-// prompts: sequence and pair of row tiles of this CTA, found by one warp.
+// prompts: sequence and pair of row tiles of a job, found by one warp.
 // Pairs are counted from each sequence's last (the most keys) to its first,
 // the KV heads of a pair next to one another.  false: no work.
-__device__ bool find_prompt(const Attend16 &p, Segment &s) {
+__device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
   const int lane = threadIdx.x & 31;
-  const int item = static_cast<int>(blockIdx.x / p.H);
-  s.h = static_cast<int>(blockIdx.x % p.H);
+  const int item = static_cast<int>(job / p.H);
+  s.h = static_cast<int>(job % p.H);
   int before = 0, highest = 0;
   bool found = false;
-  for (int b0 = 0; b0 < p.B && (!found || blockIdx.x == 0); b0 += 32) {  // block 0 looks at all bounds
+  for (int b0 = 0; b0 < p.B && (!found || job == 0); b0 += 32) {  // job 0 looks at all bounds
     const int b = b0 + lane;
     const int x = b < p.B ? p.cu[b] : 0, y = b < p.B ? p.cu[b + 1] : 0;
     // the sequences lie one behind another: none starts before an earlier bound
@@ -396,7 +420,7 @@ __device__ bool find_prompt(const Attend16 &p, Segment &s) {
     }
     const int earlier = max(highest, top);
     const bool good = x >= 0 && y >= x && y <= p.n_tok && x >= earlier;
-    if (b < p.B && !good && blockIdx.x == 0) set_status(p.status, ISOQUANT_DEVERR_SEQ_RANGE);
+    if (b < p.B && !good && job == 0) set_status(p.status, ISOQUANT_DEVERR_SEQ_RANGE);
     const int pairs = b < p.B && good ? (y - x + 2 * p.tok - 1) / (2 * p.tok) : 0;
     int incl = pairs;
 #pragma unroll
@@ -447,9 +471,9 @@ __device__ __forceinline__ uint32_t exponent_mask() {
 // there and read, weights, products; the sides' hand-overs; all products.
 struct Bars {
   uint64_t full[kMaxSlots], loaded[kMaxSlots], freed[kMaxSlots];
-  uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], o_done[2], turn[2], side1, seg_done, mma_done;
+  uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], o_done[2], turn[2], job_full[2], job_free[2], side1, seg_done, mma_done, stolen;
   // arrivals: freed and q_free take `users`, the weights p_count and a segment's end seg_count
-  __device__ void init(int slot_users, int q_users, int p_count, int seg_count) {
+  __device__ void init(int slot_users, int q_users, int p_count, int seg_count, int readers) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&loaded[i], 1);
@@ -463,14 +487,21 @@ struct Bars {
       mbar_init(&p_full[i], p_count);
       mbar_init(&o_done[i], 1);
       mbar_init(&turn[i], 1);
+      mbar_init(&job_full[i], 1);
+      mbar_init(&job_free[i], readers);
     }
     mbar_init(&side1, seg_count);
     mbar_init(&seg_done, seg_count);
     mbar_init(&mma_done, 2);
+    mbar_init(&stolen, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
 static_assert(sizeof(Bars) <= 320, "room for the barriers");
+// A prompt's piece of work as the loader hands it to the other warps.
+struct Job {
+  int kv0, rows, row0, h, n0, n1, end, pad;
+};
 // what the roles of a CTA share beside the barriers
 struct Flags {
   uint32_t tmem;
@@ -494,7 +525,7 @@ __device__ __forceinline__ float *record(const Attend16 &p, int i) {
 // caller's next __syncthreads makes them visible.
 template <uint32_t COLS>
 __device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, int slot_users, int q_users,
-                                          int p_count, int seg_count) {
+                                          int p_count, int seg_count, int readers) {
   if (threadIdx.x < 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&flags->tmem)),
                  "r"(COLS));
@@ -502,7 +533,7 @@ __device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, in
     tc_fence_before();
   }
   if (threadIdx.x == 32) {
-    bars.init(slot_users, q_users, p_count, seg_count);
+    bars.init(slot_users, q_users, p_count, seg_count, readers);
     flags->abort = flags->nonfinite = flags->done = 0;
   }
   for (int i = threadIdx.x; i < 3 * kD; i += blockDim.x) bad[i] = INT_MAX;
@@ -742,24 +773,38 @@ __global__ void __launch_bounds__(kThreads16, 1)
   Flags *flags = reinterpret_cast<Flags *>(tail + kOffFlags);
   volatile int *abort = &flags->abort, *nonfinite = &flags->nonfinite;
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
+  uint4 *stolen = reinterpret_cast<uint4 *>(tail + kOffLoc + 2 * sizeof(Job));
   const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
 
-  start_cta<512>(bars, flags, bad, 2, 2, row_warps, row_warps);
+  start_cta<512>(bars, flags, bad, 2, kPaged ? 2 : 1, row_warps, row_warps, 3 + 2 * row_warps);
   pdl_trigger();
   pdl_wait();
-  Segment prompt{};
-  bool has_prompt = false;
-  if constexpr (kPaged) {
-    locate16<kThreads16>(p, loc, loc + 8);
-  } else {
-    __syncthreads();
-    has_prompt = find_prompt(p, prompt);  // every warp by itself
-  }
+  if constexpr (kPaged) locate16<kThreads16>(p, loc, loc + 8);
+  else __syncthreads();
+  Job *jobs = reinterpret_cast<Job *>(loc);
   tc_fence_after();
   const uint32_t tmem = flags->tmem;
   auto for_segments = [&](auto &&f) {
-    if constexpr (kPaged) cache_segments(p, loc, f);
-    else if (has_prompt) f(prompt, 0u);
+    if constexpr (kPaged) {
+      cache_segments(p, loc, f);
+    } else {
+      for (uint32_t k = 0;; ++k) {
+        if (!warp_wait(&bars.job_full[k & 1], (k >> 1) & 1u, p, abort)) return;
+        const Job jb = jobs[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.job_free[k & 1]);
+        if (jb.end) return;
+        Segment s{};
+        s.h = jb.h;
+        s.kv0 = jb.kv0;
+        s.rows = s.cap = jb.rows;
+        s.row0 = jb.row0;
+        s.shift = 1;
+        s.n[0] = jb.n0;
+        s.n[1] = jb.n1;
+        if (!f(s, k)) return;
+      }
+    }
   };
 
   // registers of the four helper warps go to the softmax threads:
@@ -773,7 +818,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
     // tokens, 32 and 8 heads).
     const int x = warp;
     const uint32_t issue = lane == 0;
-    uint32_t n_p = 0, t = 0, n_turn = 0;  // weights, tiles, turns so far
+    uint32_t n_p = 0, n_q = 0, t = 0, n_turn = 0;  // weights, queries, tiles, turns so far
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity, p, abort); };
     // Both warps go through all tiles: what only the other side uses is passed,
@@ -821,7 +866,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
     };
     for_segments([&](const Segment &s, uint32_t k) {
       const int qb = kPaged ? k & 1 : x, n = kPaged ? s.n[0] : max(s.n[0], s.n[1]);
-      if (kPaged || s.n[x] > 0) wait(&bars.q_full[qb], kPaged ? (k >> 1) & 1u : 0u);
+      if (kPaged || s.n[x] > 0) wait(&bars.q_full[qb], (kPaged ? k >> 1 : n_q++) & 1u);
       if (kPaged && x >= n) arrive(&bars.q_free[qb]);
       // prompts: this side's tiles are the first s.n[x]; cache: each second
       const int first = kPaged ? x : 0, step = kPaged ? 2 : 1, last = kPaged ? n : s.n[x];
@@ -849,7 +894,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
           if (mine(i)) {
             issue_s(qb, k_slot);
             commit(&bars.freed[k_slot]);
-            if (kPaged && i + 2 >= n) commit(&bars.q_free[qb]);
+            if (i + step >= last) commit(&bars.q_free[qb]);
           } else {
             arrive(&bars.freed[k_slot]);
           }
@@ -864,35 +909,64 @@ __global__ void __launch_bounds__(kThreads16, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if constexpr (kPaged) {
       load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), 2, bars, abort);
-    } else if (has_prompt) {
-      const Segment &s = prompt;
+    } else {
       const uint32_t sq = smem_addr(smem), sr = smem_addr(ring_base);
       Loader ld(p, bars, abort);
-      // box of a Q tile: 64 dims x G heads x tok tokens
-      auto load_q = [&](int x) {
-        if (s.n[x] && lane == 0) {
-          mbar_arrive_expect_tx(&bars.q_full[x], static_cast<uint32_t>(p.R * kD * 2));
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + x * p.tok, &bars.q_full[x]);
+      uint32_t t = 0, n_q0 = 0, n_q1 = 0;
+      uint32_t job = blockIdx.x;
+      bool more = true;
+      for (uint32_t k = 0; ld.ok; ++k) {
+        Segment s{};
+        more = more && find_prompt(p, job, s);
+        // (jobs without work come last)
+        if (k > 1) ld.ok = warp_wait(&bars.job_free[k & 1], ((k >> 1) + 1) & 1u, p, abort);
+        if (!ld.ok) break;
+        if (lane == 0) {
+          jobs[k & 1] = Job{s.kv0, s.rows, s.row0, s.h, s.n[0], s.n[1], !more, 0};
+          mbar_arrive(&bars.job_full[k & 1]);
+          // the next CTA that has not started, if any: its work becomes this CTA's
+          if (more) steal_request(stolen, &bars.stolen);
         }
         __syncwarp();
-      };
-      load_q(0);
-      const int n = max(s.n[0], s.n[1]), all = all_see(p, s);
-      for (int j = 0; j < n && ld.ok; ++j) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t sl = kv ? value_slot(j, kRowSlots) : key_slot(j);
-          uint64_t *bar = ld.begin(sl, kv ? value_use(j, kRowSlots) : key_use(j), kv && (j + 1) * kTile > all, kTileBytes);
+        if (!more) break;
+        // box of a Q tile: 64 dims x G heads x tok tokens
+        auto load_q = [&](int x) {
+          if (s.n[x] == 0) return;
+          uint32_t &n_q = x ? n_q1 : n_q0;
+          if (n_q > 0) ld.ok = ld.ok && warp_wait(&bars.q_free[x], (n_q - 1) & 1u, p, abort);
+          ++n_q;
           if (lane == 0 && ld.ok) {
+            mbar_arrive_expect_tx(&bars.q_full[x], static_cast<uint32_t>(p.R * kD * 2));
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-              tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile, bar);
+              tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + x * p.tok, &bars.q_full[x]);
           }
           __syncwarp();
-          if (j == 0 && kv == 0) load_q(1);
+        };
+        const int n = max(s.n[0], s.n[1]), all = all_see(p, s);
+        for (int j = 0; j < n && ld.ok; ++j, ++t) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t sl = kv ? value_slot(t, kRowSlots) : key_slot(t);
+            uint64_t *bar =
+                ld.begin(sl, kv ? value_use(t, kRowSlots) : key_use(t), kv && (j + 1) * kTile > all, kTileBytes);
+            if (lane == 0 && ld.ok) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                tma_3d(sr + sl * kTileBytes + hf * (kTileBytes / 2), kv ? &mv : &mk, 64 * hf, s.h, s.kv0 + j * kTile,
+                       bar);
+            }
+            __syncwarp();
+            if (j == 0 && kv == 0) {
+              load_q(0);
+              load_q(1);
+            }
+          }
         }
+        // the answer (waited for even if this CTA gave up: it is a copy into its memory)
+        const bool there = __all_sync(0xffffffffu, mbar_wait(&bars.stolen, k & 1u, p.status, nullptr));
+        more = there && steal_answer(stolen, job);
+        ld.ok = ld.ok && there;
       }
       ld.drain();
     }
@@ -900,13 +974,17 @@ __global__ void __launch_bounds__(kThreads16, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if constexpr (kPaged) {
       guard_cache<T>(p, loc, ring_base, row_warps, bad, bars, flags);
-    } else if (has_prompt) {
-      const Segment &s = prompt;
-      const int all = all_see(p, s), none = none_sees(p, s, 2 * p.tok), n = max(s.n[0], s.n[1]);
-      uint32_t phases = 0;
-      bool ok = true;
-      for (int j = all / kTile; j < n && ok; ++j)
-        ok = guard_slot<T>(p, value_slot(j, kRowSlots), phases, ring_base, j * kTile, all, none, 0, 0, bad, bars, flags);
+    } else {
+      uint32_t phases = 0, t = 0;
+      for_segments([&](const Segment &s, uint32_t k) {
+        const int all = all_see(p, s), none = none_sees(p, s, 2 * p.tok), n = max(s.n[0], s.n[1]);
+        bool ok = true;
+        for (int j = all / kTile; j < n && ok; ++j)
+          ok = guard_slot<T>(p, value_slot(t + j, kRowSlots), phases, ring_base, j * kTile, all, none, k, 2 * row_warps,
+                             bad, bars, flags);
+        t += n;
+        return ok;
+      });
     }
   } else {
     // -------------------------------------------------------------- softmax
@@ -915,7 +993,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
     const int r_tok = r / p.GB, r_head = r - r_tok * p.GB;
-    uint32_t n_s = 0, n_o1 = 0;
+    uint32_t n_s = 0, n_o1 = 0, n_o = 0;
     bool ok = true;
     // one row's sum of products, times f, plus what the guards took out
     auto finish = [&](uint32_t k, int lim, float (&o)[32], int col, float f) {
@@ -958,8 +1036,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
       if (!ok) return false;
       const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
       if constexpr (!kPaged) {
-        if (n == 0) return true;
-        ok = warp_wait(&bars.o_done[x], 0, p, abort);
+        if (n == 0) {
+          if (lane == 0) atomicAdd(&flags->done, 1);
+          return true;
+        }
+        ok = warp_wait(&bars.o_done[x], n_o++ & 1u, p, abort);
         if (!ok) return false;
         tc_fence_after();
         const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -972,6 +1053,9 @@ __global__ void __launch_bounds__(kThreads16, 1)
           finish(k, lim, o, col, inv);
           if (valid) store16(dst + col, o);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) atomicAdd(&flags->done, 1);
       } else if (x == 1) {
         if (n > 0) {
           ml[r] = make_float2(sub, l);
@@ -1131,7 +1215,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
   const int soft_warps = (p.R + SR - 1) / SR * 4;  // sides without rows rest
 
-  start_cta<C::kCols>(bars, flags, bad, 1, 1, soft_warps, soft_warps);
+  start_cta<C::kCols>(bars, flags, bad, 1, 1, soft_warps, soft_warps, 1);
   // Q rows that no copy writes are zero
   for (int i = tid; i < C::kP / 16; i += C::kThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
