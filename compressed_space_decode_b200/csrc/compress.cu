@@ -9,6 +9,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "isoquant_internal.cuh"
 
 namespace isoquant {
@@ -272,13 +274,16 @@ struct LaneConsts {
   uint32_t sgn[8];
   float2 mc[4][4][2];
 };
-__device__ __forceinline__ void lane_consts(const HeadParams &hp, int q, LaneConsts &c) {
+__device__ __forceinline__ void lane_signs(const HeadParams &hp, int q, uint32_t (&sgn)[8]) {
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
     const int j = 16 * m + 2 * q;  // even: both coordinates in one sign word
     const uint32_t bits = (hp.sign_bits[j >> 5] >> (j & 31)) & 3u;
-    c.sgn[m] = ((bits & 1u) << 15) | ((bits >> 1) << 31);
+    sgn[m] = ((bits & 1u) << 15) | ((bits >> 1) << 31);
   }
+}
+__device__ __forceinline__ void lane_consts(const HeadParams &hp, int q, LaneConsts &c) {
+  lane_signs(hp, q, c.sgn);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -288,6 +293,28 @@ __device__ __forceinline__ void lane_consts(const HeadParams &hp, int q, LaneCon
       c.mc[k][r][1] = make_float2(row.z, row.w);
     }
   }
+}
+
+// The same with the blocks in shared memory (a block of warps on one head):
+// row r of block 4q + k at mc[(4 k + r) * 8 + q], so that a warp's four lane
+// groups read the same 128 bytes.  64 registers less.
+struct LaneShared {
+  uint32_t sgn[8];
+  const float4 *mc;
+};
+__device__ __forceinline__ void block_rows(const LaneConsts &c, int q, int k, int r, float2 &lo, float2 &hi) {
+  lo = c.mc[k][r][0];
+  hi = c.mc[k][r][1];
+}
+__device__ __forceinline__ void block_rows(const LaneShared &c, int q, int k, int r, float2 &lo, float2 &hi) {
+  const float4 v = c.mc[(4 * k + r) * 8 + q];
+  lo = make_float2(v.x, v.y);
+  hi = make_float2(v.z, v.w);
+}
+// a 128-thread block's blocks of head parameters; the caller synchronises
+__device__ __forceinline__ void share_blocks(const HeadParams &hp, float4 *mc) {
+  const int i = threadIdx.x, q = i & 7, r = (i >> 3) & 3, k = i >> 5;
+  mc[i] = reinterpret_cast<const float4 *>(hp.m32[4 * q + k])[r];
 }
 
 __device__ __forceinline__ float group_sum(float s) {
@@ -309,7 +336,8 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
 // coordinate 16q + i of B H D x.  The lower index of each butterfly keeps
 // a + b, the upper one a - b.  `tile` is the warp's shared tile; every lane
 // of the warp calls this together.
-__device__ __forceinline__ void rotate_two_layouts(float2 (&a)[8], const LaneConsts &c, float *tile, int grp, int q,
+template <typename C>
+__device__ __forceinline__ void rotate_two_layouts(float2 (&a)[8], const C &c, float *tile, int grp, int q,
                                                    float (&y)[16]) {
   // strides 16, 32, 64: bits 0, 1, 2 of m
 #pragma unroll
@@ -353,7 +381,9 @@ __device__ __forceinline__ void rotate_two_layouts(float2 (&a)[8], const LaneCon
   for (int k = 0; k < 4; ++k) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float2 t = __ffma2_rn(c.mc[k][r][1], b[2 * k + 1], __fmul2_rn(c.mc[k][r][0], b[2 * k]));
+      float2 lo, hi;
+      block_rows(c, q, k, r, lo, hi);
+      const float2 t = __ffma2_rn(hi, b[2 * k + 1], __fmul2_rn(lo, b[2 * k]));
       y[4 * k + r] = t.x + t.y;
     }
   }
@@ -449,31 +479,36 @@ __device__ void compress_one_fp64(const HeadParams &hp, const Codebook &cb, cons
 }
 
 
-// Warp w of the K (kv = 0) or V (kv = 1) half: rotate, quantize and pack
-// tokens strip * (w / H) .. + strip - 1 of head w % H, four at a time.
+// A warp of the K (kv = 0) or V (kv = 1) half: rotate, quantize and pack
+// tokens strip * sidx .. + strip - 1 of head h, four at a time.
 // `tile` is the warp's shared tile (kTileFloats floats).
 // ROPE: keys are rotated by position first (r), and a token whose position is
-// outside the table is skipped like one with a bad slot.
+// outside the table is skipped like one with a bad slot; the head's SO(4)
+// blocks are read from shared memory (mc).
 template <typename T, int BITS, bool ROPE = false>
-__device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uint32_t w, int lane, float *tile,
-                                              const RopeArgs &r = RopeArgs{}) {
+__device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uint32_t sidx, int h, int lane,
+                                              float *tile, const RopeArgs &r = RopeArgs{},
+                                              const float4 *mc = nullptr) {
   constexpr int kHalf = 1 << (BITS - 1);  // codes below kHalf are the negative levels
   constexpr int kPos = kHalf - 1;         // positive thresholds (the middle one is 0)
   constexpr uint32_t kAll = (1u << BITS) - 1u;
   constexpr int kW = words_for(BITS);
   const int H = g.H, n_tok = g.n_tok, ps_shift = g.ps_shift;
   const uint32_t strips = (static_cast<uint32_t>(n_tok) + g.strip - 1) / g.strip;
-  const uint32_t sidx = w / static_cast<uint32_t>(H);
   if (sidx >= strips) return;
-  const int h = static_cast<int>(w - sidx * static_cast<uint32_t>(H));
   const HeadParams &hp = g.params[h];
   const Codebook &cb = g.cb;
   const T *__restrict__ src = static_cast<const T *>(kv ? g.vin : g.kin);
   const int grp = lane >> 3, q = lane & 7;
 
   // this lane's sign masks and SO(4) blocks 4q..4q+3, for the whole strip
-  LaneConsts lc;
-  lane_consts(hp, q, lc);
+  std::conditional_t<ROPE, LaneShared, LaneConsts> lc;
+  if constexpr (ROPE) {
+    lane_signs(hp, q, lc.sgn);
+    lc.mc = mc;
+  } else {
+    lane_consts(hp, q, lc);
+  }
   // the positive thresholds (the codebook is symmetric)
   float tp[kPos];
 #pragma unroll
@@ -484,13 +519,15 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
   // the inputs and slot of the group's next vector are loaded one iteration
   // ahead, so that their latency overlaps the current vector's rotation
   RawA<T> nraw{};
-  int64_t nslot = -1, npos = 0;
+  // (positions two ahead: the table row's address waits for them)
+  int64_t nslot = -1, npos = 0, npos2 = 0;
   RopeLane nrope{};
   if (t_begin + grp < t_end) {
     nslot = g.slots[t_begin + grp];
     if constexpr (ROPE) {
       npos = r.k_pos[t_begin + grp];
-      if (kv == 0 && nslot >= 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
+      npos2 = t_begin + grp + 4 < t_end ? r.k_pos[t_begin + grp + 4] : 0;
+      if (kv == 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
     }
     load_a(src + (static_cast<int64_t>(t_begin + grp) * H + h) * kD, q, nraw);
   }
@@ -525,8 +562,9 @@ __device__ __forceinline__ void compress_warp(const CompressArgs &g, int kv, uin
     if (t + 4 < t_end) {
       nslot = g.slots[t + 4];
       if constexpr (ROPE) {
-        npos = r.k_pos[t + 4];
-        if (kv == 0 && nslot >= 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
+        npos = npos2;
+        if (kv == 0 && npos >= 0 && npos < r.num_pos) load_rope(r, npos, q, nrope);
+        if (t + 8 < t_end) npos2 = r.k_pos[t + 8];
       }
       load_a(src + (static_cast<int64_t>(t + 4) * H + h) * kD, q, nraw);
     }
@@ -675,7 +713,8 @@ __global__ void __launch_bounds__(kCompressWarps * 32, kCompressBlocksPerSm) k_c
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5;
-  compress_warp<T, BITS>(g, blockIdx.y, blockIdx.x * (blockDim.x >> 5) + warp, threadIdx.x & 31, tile[warp]);
+  const uint32_t w = blockIdx.x * (blockDim.x >> 5) + warp, sidx = w / static_cast<uint32_t>(g.H);
+  compress_warp<T, BITS>(g, blockIdx.y, sidx, static_cast<int>(w - sidx * g.H), threadIdx.x & 31, tile[warp]);
 }
 
 // Debug export of the fast path's fp32 z: the same lane-group layouts and
@@ -768,7 +807,8 @@ __global__ void __launch_bounds__(256) k_decode_prep(const CompressArgs c, const
   const int bx = static_cast<int>(blockIdx.x);
   if (bx < 2 * nbc) {
     const int kv = bx >= nbc ? 1 : 0;
-    compress_warp<T, BITS>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * (blockDim.x >> 5) + warp, lane, tile[warp]);
+    const uint32_t w = static_cast<uint32_t>(bx - kv * nbc) * (blockDim.x >> 5) + warp, sidx = w / static_cast<uint32_t>(c.H);
+    compress_warp<T, BITS>(c, kv, sidx, static_cast<int>(w - sidx * c.H), lane, tile[warp]);
   } else {
     rotate_warp<T>(r, static_cast<uint32_t>(bx - 2 * nbc) * (blockDim.x >> 5) + warp, lane);
   }
@@ -786,35 +826,44 @@ __device__ __forceinline__ void store8(float *dst, const float *v) {
                : "memory");
 }
 template <typename T>
-__device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t w, int lane, float *tile,
-                                             const RopeArgs &r, uint32_t *status) {
-  const uint32_t H = static_cast<uint32_t>(g.Hq / g.G), total = static_cast<uint32_t>(g.n_rows) * g.G;
-  const uint32_t sidx = w / H;
-  const int h = static_cast<int>(w - sidx * H);
+__device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t sidx, int h, int lane, float *tile,
+                                             const RopeArgs &r, const float4 *mc, uint32_t *status) {
+  const uint32_t total = static_cast<uint32_t>(g.n_rows) * g.G;
   const uint32_t begin = sidx * g.strip;
   if (begin >= total) return;
   const uint32_t end = min(begin + g.strip, total);
   const int grp = lane >> 3, q = lane & 7;
-  LaneConsts lc;
-  lane_consts(g.params[h], q, lc);
+  LaneShared lc;
+  lane_signs(g.params[h], q, lc.sgn);
+  lc.mc = mc;
   const T *__restrict__ src = static_cast<const T *>(g.q) + static_cast<int64_t>(h) * g.G * kD;
   float *__restrict__ dst = g.out + static_cast<int64_t>(h) * g.G * kD + 16 * q;
   const bool wide = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0;
-  // the next vector's inputs and table row are loaded one iteration ahead
+  // the next vector's inputs and table row are loaded one iteration ahead, its
+  // position two (the row's address waits for it)
   RawA<T> raw{};
   RopeLane rope{};
-  uint32_t row = 0, head = 0;  // of the vector in hand
+  uint32_t row = 0, head = 0, nrow = 0, nhead = 0;  // of the vector in hand, and behind it
+  int64_t npos = 0;
   bool good = false;
-  auto fetch = [&](uint32_t e) {
-    row = e / static_cast<uint32_t>(g.G);
-    head = e - row * g.G;
-    const int64_t pos = r.q_pos[row];
-    good = pos >= 0 && pos < r.num_pos;
-    if (good) load_rope(r, pos, q, rope);
+  auto locate = [&](uint32_t e) {
+    nrow = e / static_cast<uint32_t>(g.G);
+    nhead = e - nrow * g.G;
+    npos = r.q_pos[nrow];
+  };
+  auto fetch = [&]() {
+    row = nrow;
+    head = nhead;
+    good = npos >= 0 && npos < r.num_pos;
+    if (good) load_rope(r, npos, q, rope);
     else if (q == 0) set_status(status, ISOQUANT_DEVERR_POS_RANGE);
     load_a(src + (static_cast<int64_t>(row) * g.Hq + head) * kD, q, raw);
   };
-  if (begin + grp < end) fetch(begin + grp);
+  if (begin + grp < end) {
+    locate(begin + grp);
+    fetch();
+  }
+  if (begin + grp + 4 < end) locate(begin + grp + 4);
   for (uint32_t e0 = begin; e0 < end; e0 += 4) {
     const uint32_t e = e0 + grp;
     const bool live = e < end, zero = !good;
@@ -824,7 +873,8 @@ __device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t w, in
     unpack_a(raw, none, a);
     rope_a(r, rope, a);
     sign_a(lc.sgn, a);
-    if (e + 4 < end) fetch(e + 4);
+    if (e + 4 < end) fetch();
+    if (e + 8 < end) locate(e + 8);
     float y[16];
     rotate_two_layouts(a, lc, tile, grp, q, y);
     if (live) {
@@ -841,22 +891,27 @@ __device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t w, in
   }
 }
 
+// A block's four warps take strips of one head.
+constexpr int kRopeWarps = 4;
+constexpr int kRopeBlocksPerSm = 4;
 template <typename T, int BITS>
-__global__ void __launch_bounds__(kCompressWarps * 32, kCompressBlocksPerSm)
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
     k_decode_prep_rope(const CompressArgs c, const RotateArgs r, const RopeArgs rope, int nbc) {
-  __shared__ __align__(16) float tile[kCompressWarps][kTileFloats];
+  __shared__ __align__(16) float tile[kRopeWarps][kTileFloats];
+  __shared__ __align__(16) float4 mc[128];
   pdl_trigger();
   pdl_wait();
   const uint32_t warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int bx = static_cast<int>(blockIdx.x);
-  if (bx < 2 * nbc) {
-    const int kv = bx >= nbc ? 1 : 0;
-    compress_warp<T, BITS, true>(c, kv, static_cast<uint32_t>(bx - kv * nbc) * kCompressWarps + warp, lane, tile[warp],
-                                 rope);
-  } else {
-    rotate_strip<T>(r, static_cast<uint32_t>(bx - 2 * nbc) * kCompressWarps + warp, lane, tile[warp], rope, c.status);
-  }
+  const int kv = bx >= nbc ? 1 : 0;
+  const bool keys = bx < 2 * nbc;
+  const uint32_t i = static_cast<uint32_t>(keys ? bx - kv * nbc : bx - 2 * nbc), row = i / static_cast<uint32_t>(c.H);
+  const int h = static_cast<int>(i - row * c.H);
+  share_blocks(c.params[h], mc);
+  __syncthreads();
+  if (keys) compress_warp<T, BITS, true>(c, kv, row * kRopeWarps + warp, h, lane, tile[warp], rope, mc);
+  else rotate_strip<T>(r, row * kRopeWarps + warp, h, lane, tile[warp], rope, mc, c.status);
 }
 
 }  // namespace
@@ -1027,21 +1082,27 @@ cudaError_t launch_decode_prep_rope(const isoquant_ctx *ctx, const isoquant_cach
                                     const void *v, int n_tok, const int64_t *slot_mapping, const int64_t *k_pos,
                                     const void *q, int dtype, int n_rows, int num_q_heads, const int64_t *q_pos,
                                     const isoquant_rope *rope, float *q_rot, cudaStream_t stream) {
-  const int64_t nbc = compress_blocks(ctx, n_tok, kCompressWarps);
-  const CompressArgs c = compress_args(ctx, cache, k, v, n_tok, slot_mapping);
+  CompressArgs c = compress_args(ctx, cache, k, v, n_tok, slot_mapping);
   RotateArgs r = rotate_args(ctx, q, n_rows, num_q_heads, q_rot);
-  // as many strips as the SMs hold warps, of 4 to 64 vectors
-  const int64_t vectors = static_cast<int64_t>(n_rows) * num_q_heads;
-  const int64_t resident = static_cast<int64_t>(ctx->num_sms) * kCompressWarps * kCompressBlocksPerSm;
-  const int64_t even = (vectors / resident) & ~int64_t(3);
-  r.strip = static_cast<uint32_t>(even < 4 ? 4 : even > 64 ? 64 : even);
-  const int64_t strips = (static_cast<int64_t>(n_rows) * r.G + r.strip - 1) / r.strip * ctx->num_kv_heads;
-  const int64_t nbr = (strips + kCompressWarps - 1) / kCompressWarps;
-  const int64_t blocks = 2 * nbc + nbr;
+  // strips of 4 to 64 vectors of a head, as many as the SMs hold warps
+  const int H = ctx->num_kv_heads;
+  const int64_t resident = static_cast<int64_t>(ctx->num_sms) * kRopeWarps * kRopeBlocksPerSm;
+  auto strip_of = [&](int64_t vectors) {
+    const int64_t even = (vectors / resident) & ~int64_t(3);
+    return static_cast<int>(even < 4 ? 4 : even > 64 ? 64 : even);
+  };
+  auto blocks_of = [&](int64_t per_head, int64_t strip) {
+    const int64_t strips = (per_head + strip - 1) / strip;
+    return (strips + kRopeWarps - 1) / kRopeWarps * H;
+  };
+  c.strip = strip_of(static_cast<int64_t>(n_tok) * H);
+  r.strip = static_cast<uint32_t>(strip_of(static_cast<int64_t>(n_rows) * num_q_heads));
+  const int64_t nbc = blocks_of(n_tok, c.strip);
+  const int64_t blocks = 2 * nbc + blocks_of(static_cast<int64_t>(n_rows) * r.G, r.strip);
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const RopeArgs ra{rope->cos_sin, k_pos, q_pos, rope->num_positions, rope->rot_dim, rope->interleaved};
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kCompressWarps * 32);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kRopeWarps * 32);
   const int nb = static_cast<int>(nbc);
   switch (ctx->codebook.bits) {
     case 2: return launch_prep_rope_t<2>(dtype, grid, block, stream, c, r, ra, nb);
