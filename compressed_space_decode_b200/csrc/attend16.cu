@@ -62,6 +62,7 @@ constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (referen
 
 struct Attend16 {
   int H, Hq, G, GB, chunks, tok, R, B, nq, causal;  // GB: heads of a row tile (G, or 128 of a larger group)
+  int rts;                                          // cache: row tiles of a sequence and KV head
   float c;                                          // softmax scale * log2(e)
   const int32_t *cu;                                // prompts
   int n_tok;
@@ -104,6 +105,10 @@ __device__ __forceinline__ float with_nonfinite(float o, const int *bad, int d, 
   if (bad[d] < lim) o += INFINITY;
   if (bad[kD + d] < lim) o -= INFINITY;
   return bad[2 * kD + d] < lim ? NAN : o;
+}
+
+__device__ __forceinline__ void fetch_map(const CUtensorMap &map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
 }
 
 // shared-memory matrix descriptor, 128-byte swizzle, strides in 16-byte units
@@ -289,28 +294,34 @@ struct Segment {
 struct Unit {
   int b, rt, L, cap, row0, chunk, nt;
   __device__ void set(const Attend16 &p, int u) {
-    const int rts = (p.nq + p.tok - 1) / p.tok * p.chunks;
-    b = u / rts;
-    rt = u - b * rts;
+    b = p.rts == 1 ? u : u / p.rts;
+    rt = u - b * p.rts;
     L = p.seq_lens[b];
     const int64_t room = static_cast<int64_t>(p.max_pages) << p.ps_shift;
     cap = max(0, static_cast<int>(min(static_cast<int64_t>(L), room)));
-    row0 = rt / p.chunks * p.tok;
-    chunk = rt % p.chunks;
+    row0 = p.chunks == 1 ? rt * p.tok : rt / p.chunks * p.tok;
+    chunk = p.chunks == 1 ? 0 : rt % p.chunks;
     const int last = min(p.nq, row0 + p.tok) - 1;
     const int64_t hz = p.causal ? min(static_cast<int64_t>(cap), static_cast<int64_t>(L) - p.nq + last + 1) : cap;
     nt = max(1, static_cast<int>((hz + kTile - 1) / kTile));
   }
 };
 
+// a / b for a >= 0, b > 0: 32-bit division where it does (a 64-bit one takes
+// some hundred cycles, and a call of few tiles waits for a handful of them)
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The CTA's part [gs, ge) of all tiles, and the (unit, tile offset) where it
 // starts.  loc: {gs, ge, unit, offset, total}; ends with __syncthreads.
 template <int NT>
 __device__ void locate16(const Attend16 &p, int64_t *loc, int64_t *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int U = p.B * ((p.nq + p.tok - 1) / p.tok * p.chunks);
-  const int u0 = static_cast<int>(static_cast<int64_t>(U) * tid / NT),
-            u1 = static_cast<int>(static_cast<int64_t>(U) * (tid + 1) / NT);
+  const int U = p.B * p.rts;
+  const int u0 = static_cast<int>(div64(static_cast<int64_t>(U) * tid, NT)),
+            u1 = static_cast<int>(div64(static_cast<int64_t>(U) * (tid + 1), NT));
   int64_t mine = 0;
   Unit un;
   for (int u = u0; u < u1; ++u) {
@@ -333,7 +344,7 @@ __device__ void locate16(const Attend16 &p, int64_t *loc, int64_t *scratch) {
   }
   const int64_t excl = before + incl - mine;
   const int64_t N = min(static_cast<int64_t>(p.n_cta), total), c = blockIdx.x;
-  const int64_t gs = c < N ? total * c / N : 0, ge = c < N ? total * (c + 1) / N : 0;
+  const int64_t gs = c < N ? div64(total * c, N) : 0, ge = c < N ? div64(total * (c + 1), N) : 0;
   if (tid == 0) {
     loc[0] = gs;
     loc[1] = ge;
@@ -366,7 +377,7 @@ struct Walk16 {
     if (g < ge) {
       u = static_cast<int>(loc[2]);
       un.set(p, u);
-      h = static_cast<int>(loc[3] / un.nt);
+      h = static_cast<int>(div64(loc[3], un.nt));
       j = static_cast<int>(loc[3] - static_cast<int64_t>(h) * un.nt);
     }
   }
@@ -751,7 +762,7 @@ __device__ void write_plan(const Attend16 &p, const int64_t *loc) {
     if (s.starts && !s.whole) {
       const int64_t N = min(static_cast<int64_t>(p.n_cta), total);
       const int64_t last = ge + (wk.un.nt - wk.j) - 1;  // the segment's last tile
-      plan = make_int2(s.id, static_cast<int>(((last + 1) * N + total - 1) / total - 1));
+      plan = make_int2(s.id, static_cast<int>(div64((last + 1) * N + total - 1, total) - 1));
     }
   }
   p.plan[blockIdx.x] = plan;
@@ -777,6 +788,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
   const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
 
   start_cta<512>(bars, flags, bad, 2, kPaged ? 2 : 1, row_warps, row_warps, 3 + 2 * row_warps);
+  if (tid == 64) {
+    fetch_map(mq);
+    fetch_map(mk);
+    if (!kPaged) fetch_map(mv);
+  }
   pdl_trigger();
   pdl_wait();
   if constexpr (kPaged) locate16<kThreads16>(p, loc, loc + 8);
@@ -1219,6 +1235,10 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
   // Q rows that no copy writes are zero
   for (int i = tid; i < C::kP / 16; i += C::kThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (tid == 64) {
+    fetch_map(mq);
+    fetch_map(mk);
+  }
   pdl_trigger();
   pdl_wait();
   locate16<C::kThreads>(p, loc, loc + 8);
@@ -1477,8 +1497,7 @@ __global__ void __launch_bounds__(128) k_combine16(const Attend16 p) {
   if (plan.x < 0) return;
   const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int u = plan.x / p.H, h = plan.x - u * p.H;
-  const int rts = (p.nq + p.tok - 1) / p.tok * p.chunks;
-  const int b = u / rts, rt = u - b * rts;
+  const int b = u / p.rts, rt = u - b * p.rts;
   const int qi = rt / p.chunks * p.tok + r / p.GB, hq = rt % p.chunks * kTile + r % p.GB;
   if (r >= p.R || qi >= p.nq || hq >= p.G) return;
   const int first = blockIdx.x, count = plan.y - first + 1;
@@ -1596,6 +1615,7 @@ void paged_rows(Attend16 &p, const AttendShape &s) {
   row_tiles(p, s.group);
   if (p.tok > s.nq) p.tok = s.nq;
   p.R = p.tok * p.GB;
+  p.rts = (s.nq + p.tok - 1) / p.tok * p.chunks;
   p.row_stride = (p.R + 1) / 2 * 2;
 }
 
