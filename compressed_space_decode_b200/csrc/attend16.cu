@@ -141,22 +141,29 @@ __device__ constexpr uint32_t idesc16(int n, int a_mn, int b_mn) {
   return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) |
          (static_cast<uint32_t>(b_mn) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
-// (the whole warp runs the issuing code, so that its descriptors stay in
-// uniform registers; the thread with `issue` set issues)
-__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+// The whole warp runs the issuing code; the thread with `issue` set issues.
+// Only a descriptor's low word changes from product to product (addresses stay
+// below 2^18), so the high words are converted once: the fewer instructions
+// a product takes, the less its warp's neighbours delay it.
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint32_t a_add, uint64_t b,
+                                       uint32_t b_add, uint32_t idesc, uint32_t acc) {
+  const uint32_t al = static_cast<uint32_t>(a) + a_add, ah = static_cast<uint32_t>(a >> 32);
+  const uint32_t bl = static_cast<uint32_t>(b) + b_add, bh = static_cast<uint32_t>(b >> 32);
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, {%7, %7, %7, %7}, p;\n\t}\n" ::"r"(d),
+      "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t b_add,
+                                       uint32_t idesc, uint32_t acc) {
+  const uint32_t bl = static_cast<uint32_t>(b) + b_add, bh = static_cast<uint32_t>(b >> 32);
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, {%6, %6, %6, %6}, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(bl), "r"(bh), "r"(idesc), "r"(acc), "r"(0u), "r"(issue)
       : "memory");
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -309,7 +316,8 @@ struct Unit {
     b = p.rts == 1 ? u : u / p.rts;
     rt = u - b * p.rts;
     L = p.seq_lens[b];
-    const int64_t room = static_cast<int64_t>(p.max_pages) << p.ps_shift;
+    // (places behind a row's last tile are counted in 32 bits too)
+    const int64_t room = min(static_cast<int64_t>(p.max_pages) << p.ps_shift, static_cast<int64_t>(INT_MAX - 2 * kTile));
     cap = max(0, static_cast<int>(min(static_cast<int64_t>(L), room)));
     row0 = p.chunks == 1 ? rt * p.tok : rt / p.chunks * p.tok;
     chunk = p.chunks == 1 ? 0 : rt % p.chunks;
@@ -909,8 +917,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
       const uint64_t a = dQ + static_cast<uint64_t>(qb) * (kTileBytes >> 4), b = dK + sl * (kTileBytes >> 4);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        mma_ss(issue, tmem + 128 * x, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
-               b + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3), idesc16<T>(kTile, 0, 0), q > 0);
+        mma_ss(issue, tmem + 128 * x, a, (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3), b,
+               (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3), idesc16<T>(kTile, 0, 0), q > 0);
       umma_commit_by(issue, &bars.s_full[x]);
     };
     auto issue_pv = [&](uint32_t sl, bool first) {
@@ -919,12 +927,12 @@ __global__ void __launch_bounds__(kThreads16, 1)
       const uint64_t b = dV + sl * (kTileBytes >> 4);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, b + 128 * q, idesc16<T>(kTile, 0, 1),
+        mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, b, 128 * q, idesc16<T>(kTile, 0, 1),
                !first || q > 0);
       if constexpr (kLo) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * q, b + 128 * q, idesc16<T>(kTile, 0, 1), 1);
+          mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 64 + 8 * q, b, 128 * q, idesc16<T>(kTile, 0, 1), 1);
       }
     };
     for_segments([&](const Segment &s, uint32_t k) {
@@ -1222,7 +1230,7 @@ struct Cols {
   // Each row's reference, the score above which it moves, what is added to a
   // score's logarithm, what an O column is multiplied by, and four warps'
   // maxima or sums.
-  static constexpr int kRefs = kTail + kTailBytes;
+  static constexpr int kRefs = kTail + kTailBytes + 64;  // (locate's scratch: a word of 8 bytes per warp)
   static constexpr int kLimits = kRefs + NR * 4;
   static constexpr int kSubs = kLimits + NR * 4;
   static constexpr int kFactor = kSubs + NR * 4;
@@ -1231,6 +1239,7 @@ struct Cols {
   static constexpr uint32_t kColO = 2 * NR;            // S^T buffers at 0 and NR
   static constexpr uint32_t kCols = kColO + kN <= 64 ? 64 : kColO + kN <= 128 ? 128 : 256;
   static_assert(kRing % 1024 == 0 && kBytes <= 227 * 1024 && kColO + kN <= kCols, "layout");
+  static_assert(64 + kThreads / 32 * 8 <= 160 + 64, "locate's scratch");
 };
 
 // barrier of a side's 128 threads with a vote
@@ -1319,8 +1328,8 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
             const uint64_t a = dK + sl * (kTileBytes >> 4), b = dQ + qb * (C::kQBytes >> 4);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              mma_ss(issue, tmem + buf * NR, a + (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3),
-                     b + (q >> 2) * (C::kQBytes >> 5) + 2 * (q & 3), idesc16<T>(NR, 0, 0), q > 0);
+              mma_ss(issue, tmem + buf * NR, a, (q >> 2) * (kTileBytes >> 5) + 2 * (q & 3), b,
+                     (q >> 2) * (C::kQBytes >> 5) + 2 * (q & 3), idesc16<T>(NR, 0, 0), q > 0);
           }
           commit(&bars.s_full[buf]);
           commit(&bars.freed[sl]);
@@ -1337,7 +1346,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
             const uint64_t a = dV + sl * (kTileBytes >> 4), b = dP + tiles % C::kPBufs * (C::kPBytes >> 4);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              mma_ss(issue, tmem + C::kColO, a + 128 * q, b + 16 * q, idesc16<T>(C::kN, 1, 1), i > 0 || q > 0);
+              mma_ss(issue, tmem + C::kColO, a, 128 * q, b, 16 * q, idesc16<T>(C::kN, 1, 1), i > 0 || q > 0);
           }
           commit(&bars.freed[sl]);
           commit(&bars.o_done[buf]);
@@ -1638,6 +1647,9 @@ cudaError_t launch_tiles(int device, int threads, int smem, unsigned grid, cudaS
   }
   return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
 }
+static_assert(2 * kTileBytes + kRowSlots * kTileBytes + kOffMl + kTile * 8 <= 227 * 1024 && 64 + kThreads16 / 32 * 8 <= 160 &&
+                  2 * sizeof(Job) + 16 <= 160,
+              "shared memory of k_attend16");
 int rows_smem(const Attend16 &p) { return 4 * p.q_half + p.slots * kTileBytes + kOffMl + kTile * 8; }
 
 template <typename T, int NR>

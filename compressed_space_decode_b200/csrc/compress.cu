@@ -894,6 +894,7 @@ __device__ __forceinline__ void rotate_strip(const RotateArgs &g, uint32_t sidx,
 // A block's four warps take strips of one head.
 constexpr int kRopeWarps = 4;
 constexpr int kRopeBlocksPerSm = 4;
+static_assert(kRopeWarps * 32 == 128, "share_blocks");
 template <typename T, int BITS>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
     k_decode_prep_rope(const CompressArgs c, const RotateArgs r, const RopeArgs rope, int nbc) {
