@@ -75,6 +75,7 @@ constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (referen
 struct Attend16 {
   int H, Hq, G, GB, chunks, tok, R, B, nq, causal;  // GB: heads of a row tile (G, or 128 of a larger group)
   int rts;                                          // cache: row tiles of a sequence and KV head
+  int sides;                                        // prompts: row tiles of a job (1: the sides share its key tiles)
   float c;                                          // softmax scale * log2(e)
   const int32_t *cu;                                // prompts
   int n_tok;
@@ -454,7 +455,7 @@ __device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
     const int earlier = max(highest, top);
     const bool good = x >= 0 && y >= x && y <= p.n_tok && x >= earlier;
     if (b < p.B && !good && job == 0) set_status(p.status, ISOQUANT_DEVERR_SEQ_RANGE);
-    const int pairs = b < p.B && good ? (y - x + 2 * p.tok - 1) / (2 * p.tok) : 0;
+    const int pairs = b < p.B && good ? (y - x + p.sides * p.tok - 1) / (p.sides * p.tok) : 0;
     if (p.B <= 32) {
       if (item >= __reduce_add_sync(0xffffffffu, pairs)) return false;
       int pair = 0;
@@ -484,7 +485,7 @@ __device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
       s.b = src;
       s.kv0 = __shfl_sync(0xffffffffu, x, src);
       s.rows = __shfl_sync(0xffffffffu, y - x, src);
-      s.row0 = __shfl_sync(0xffffffffu, pair, src) * 2 * p.tok;
+      s.row0 = __shfl_sync(0xffffffffu, pair, src) * p.sides * p.tok;
       found = true;
       break;
     }
@@ -502,7 +503,7 @@ __device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
       s.kv0 = __shfl_sync(0xffffffffu, x, src);
       s.rows = __shfl_sync(0xffffffffu, y - x, src);
       const int pair = __shfl_sync(0xffffffffu, first + pairs - 1 - item, src);
-      s.row0 = pair * 2 * p.tok;
+      s.row0 = pair * p.sides * p.tok;
       found = true;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -516,7 +517,11 @@ __device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int lo = s.row0 + x * p.tok, hi = min(s.rows, lo + p.tok);
-    s.n[x] = lo < s.rows ? ((p.causal ? hi : s.rows) + kTile - 1) / kTile : 0;
+    s.n[x] = x < p.sides && lo < s.rows ? ((p.causal ? hi : s.rows) + kTile - 1) / kTile : 0;
+  }
+  if (p.sides == 1) {
+    s.n[1] = s.n[0] >> 1;
+    s.n[0] -= s.n[1];
   }
   return true;
 }
@@ -823,9 +828,11 @@ __device__ void write_plan(const Attend16 &p, const int64_t *loc) {
   p.plan[blockIdx.x] = plan;
 }
 
-// kPaged: the cache's form for more than 64 rows, else prompts.  kLo: bf16
+// kPaged: the cache's form for more than 64 rows, else prompts.  kAlternate: the
+// sides take alternate key tiles of the same rows (the cache, few prompts),
+// else key tiles in common and rows of their own.  kLo: bf16
 // weights as two operands (16 bits), so that the result is off by one rounding.
-template <typename T, bool kPaged>
+template <typename T, bool kPaged, bool kAlternate>
 __global__ void __launch_bounds__(kThreads16, 1)
     k_attend16(const Attend16 p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv) {
@@ -841,6 +848,10 @@ __global__ void __launch_bounds__(kThreads16, 1)
   int64_t *loc = reinterpret_cast<int64_t *>(tail + kOffLoc);
   uint4 *stolen = reinterpret_cast<uint4 *>(tail + kOffLoc + 2 * sizeof(Job));
   const int row_warps = (p.R + 31) / 32;  // warps of a side that hold rows
+  // a segment's key tiles
+  auto tiles = [&](const Segment &s) {
+    return kPaged ? s.n[0] : kAlternate ? s.n[0] + s.n[1] : max(s.n[0], s.n[1]);
+  };
 
   start_cta<512>(bars, flags, bad, 2, kPaged ? 2 : 1, row_warps, row_warps, 3 + 2 * row_warps);
   if (tid == 64) {
@@ -936,12 +947,12 @@ __global__ void __launch_bounds__(kThreads16, 1)
       }
     };
     for_segments([&](const Segment &s, uint32_t k) {
-      const int qb = kPaged ? k & 1 : x, n = kPaged ? s.n[0] : max(s.n[0], s.n[1]);
+      const int qb = kPaged ? k & 1 : x, n = tiles(s);
       if (kPaged || s.n[x] > 0) wait(&bars.q_full[qb], (kPaged ? k >> 1 : n_q++) & 1u);
       if (kPaged && x >= n) arrive(&bars.q_free[qb]);
-      // prompts: this side's tiles are the first s.n[x]; cache: each second
-      const int first = kPaged ? x : 0, step = kPaged ? 2 : 1, last = kPaged ? n : s.n[x];
-      auto mine = [&](int i) { return i < last && (!kPaged || (i & 1) == x); };
+      // this side's tiles: each second, or the first s.n[x]
+      const int first = kAlternate ? x : 0, step = kAlternate ? 2 : 1, last = kAlternate ? n : s.n[x];
+      auto mine = [&](int i) { return i < last && (!kAlternate || (i & 1) == x); };
       for (int i = 0; i < n + step && ok; ++i) {
         // the product of tile i - step, then the scores of tile i: both tiles first
         const bool has_v = i >= step;
@@ -1010,11 +1021,12 @@ __global__ void __launch_bounds__(kThreads16, 1)
             mbar_arrive_expect_tx(&bars.q_full[x], static_cast<uint32_t>(p.R * kD * 2));
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-              tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + x * p.tok, &bars.q_full[x]);
+              tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + (kAlternate ? 0 : x * p.tok),
+                     &bars.q_full[x]);
           }
           __syncwarp();
         };
-        const int n = max(s.n[0], s.n[1]), all = all_see(p, s);
+        const int n = tiles(s), all = all_see(p, s);
         for (int j = 0; j < n && ld.ok; ++j, ++t) {
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
@@ -1048,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
     } else {
       uint32_t phases = 0, t = 0;
       for_segments([&](const Segment &s, uint32_t k) {
-        const int all = all_see(p, s), none = none_sees(p, s, 2 * p.tok), n = max(s.n[0], s.n[1]);
+        const int all = all_see(p, s), none = none_sees(p, s, p.sides * p.tok), n = tiles(s);
         bool ok = true;
         for (int j = all / kTile; j < n && ok; ++j)
           ok = guard_slot<T>(p, value_slot(t + j, kRowSlots), phases, ring_base, j * kTile, all, none, k, 2 * row_warps,
@@ -1084,19 +1096,19 @@ __global__ void __launch_bounds__(kThreads16, 1)
     };
     if ((warp & 3) < row_warps) for_segments([&](const Segment &s, uint32_t k) {
       const int n = kPaged ? (s.n[0] + 1 - x) >> 1 : s.n[x];
-      const int qi = s.row0 + (kPaged ? 0 : x * p.tok) + r_tok;
+      const int qi = s.row0 + (kAlternate ? 0 : x * p.tok) + r_tok;
       const int hq = s.chunk * kTile + r_head;
       const bool valid = r < p.R && qi < s.rows && hq < p.G;
       const int lim = valid ? s.limit(qi, p.causal) : 0;
       float ref = -INFINITY, l = 0.f;
       for (int i = 0; i < n && ok; ++i) {
-        const int t0 = (s.j0 + (kPaged ? 2 * i + x : i)) * kTile;
+        const int t0 = (s.j0 + (kAlternate ? 2 * i + x : i)) * kTile;
         ok = warp_wait(&bars.s_full[x], n_s & 1u, p, abort);
         ++n_s;
         // Side 1's O and sums are merged by side 0 before it writes them again.
         // (Its scores are here, so side 0 is past segment k - 2 and the parity
         // is that of k - 1.)
-        if (kPaged && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
+        if (kAlternate && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
         if (!ok) break;
         tc_fence_after();
         softmax_tile<T, kLo>(ts, to, p.c, lim - t0, i == 0, ref, l);
@@ -1106,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
       }
       if (!ok) return false;
       const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
-      if constexpr (!kPaged) {
+      if (!kAlternate) {
         if (n == 0) {
           if (lane == 0) atomicAdd(&flags->done, 1);
           return true;
@@ -1128,13 +1140,14 @@ __global__ void __launch_bounds__(kThreads16, 1)
         __syncwarp();
         if (lane == 0) atomicAdd(&flags->done, 1);
       } else if (x == 1) {
-        if (n > 0) {
-          ml[r] = make_float2(sub, l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.side1);
+        if (n > 0) ml[r] = make_float2(sub, l);
+        __syncwarp();
+        if (lane == 0) {
+          if (n > 0) mbar_arrive(&bars.side1);
+          if (!kPaged) atomicAdd(&flags->done, 1);
         }
       } else {
-        const bool both = s.n[0] > 1;
+        const bool both = tiles(s) > 1, whole = !kPaged || s.whole;
         ok = warp_wait(&bars.o_done[0], k & 1u, p, abort);
         if (both) {
           ok = ok && warp_wait(&bars.o_done[1], n_o1 & 1u, p, abort) &&
@@ -1156,9 +1169,10 @@ __global__ void __launch_bounds__(kThreads16, 1)
         const float inv = l != 0.f ? 1.f / l : 0.f;
         // whole: the result; else a record for the combine kernel
         float *rec = record(p, 2 * blockIdx.x + (s.starts ? 1 : 0));
-        T *dst = static_cast<T *>(p.out) + ((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq +
+        const int64_t row = kPaged ? static_cast<int64_t>(s.b) * p.nq + qi : s.kv0 + qi;
+        T *dst = static_cast<T *>(p.out) + (row * p.Hq +
                                             static_cast<int64_t>(s.h) * p.G + hq) * kD;
-        if (valid && !s.whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
+        if (valid && !whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
 #pragma unroll
         for (int col = 0; col < kD; col += 32) {
           float o[32];
@@ -1169,9 +1183,9 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
           }
-          finish(k, lim, o, col, s.whole ? inv : 1.f);
+          finish(k, lim, o, col, whole ? inv : 1.f);
           if (valid) {
-            if (s.whole) {
+            if (whole) {
               store16(dst + col, o);
             } else {
 #pragma unroll
@@ -1666,7 +1680,13 @@ cudaError_t launch_cache(Attend16 p, const CUtensorMap &mq, const CUtensorMap &m
   if (p.R <= 64) return launch_cols<T, 64>(p, mq, mk, grid, stream);
   p.slots = kRowSlots;
   p.q_half = kTileBytes / 2;
-  return launch_tiles<k_attend16<T, true>>(p.device, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
+  return launch_tiles<k_attend16<T, true, true>>(p.device, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mk);
+}
+
+template <typename T, bool kAlternate>
+cudaError_t launch_prompt(const Attend16 &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                          unsigned grid, cudaStream_t stream) {
+  return launch_tiles<k_attend16<T, false, kAlternate>>(p.device, kThreads16, rows_smem(p), grid, stream, p, mq, mk, mv);
 }
 
 // the cache's row tiles: rows, and the stride of a record's rows
@@ -1706,13 +1726,22 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
       !encode_rows(&mk, dtype, k, n_tok, p.H, k_stride, 1, kTile) ||
       !encode_rows(&mv, dtype, v, n_tok, p.H, v_stride, 1, kTile))
     return cudaErrorInvalidValue;
-  // pairs of row tiles: no more than one per 2 tok tokens and one per sequence
-  const int64_t grid = (static_cast<int64_t>(n_tok) / (2 * p.tok) + batch) * p.H;
+  // jobs: no more than one per `sides` row tiles and one per sequence
+  auto jobs = [&](int sides) { return (static_cast<int64_t>(n_tok) / (sides * p.tok) + batch) * p.H; };
+  // Where two-sided jobs would leave SMs idle, jobs of one row tile whose key
+  // tiles the sides share are half as long (7237 tokens, 2 and 1 heads, 57
+  // jobs: 147 -> 96 us; 114 jobs 47.9 -> 44.8, 126 jobs 82 -> 80), but read each
+  // key tile twice as often (136 short jobs 23.3 -> 25.6, 376 jobs 105 -> 123).
+  p.sides = jobs(2) < ctx->num_sms * 3 / 4 ? 1 : 2;
+  const int64_t grid = jobs(p.sides);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(grid);
-  return dtype == ISOQUANT_BF16
-             ? launch_tiles<k_attend16<__nv_bfloat16, false>>(p.device, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv)
-             : launch_tiles<k_attend16<__half, false>>(p.device, kThreads16, rows_smem(p), g, stream, p, mq, mk, mv);
+  const bool bf = dtype == ISOQUANT_BF16;
+  if (p.sides == 1)
+    return bf ? launch_prompt<__nv_bfloat16, true>(p, mq, mk, mv, g, stream)
+              : launch_prompt<__half, true>(p, mq, mk, mv, g, stream);
+  return bf ? launch_prompt<__nv_bfloat16, false>(p, mq, mk, mv, g, stream)
+            : launch_prompt<__half, false>(p, mq, mk, mv, g, stream);
 }
 
 size_t dense_workspace_bytes(const isoquant_ctx *ctx, const AttendShape &s) {

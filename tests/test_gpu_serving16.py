@@ -233,3 +233,59 @@ def test_thousands_of_prompts(cuda_lib, causal):
         a, z = int(at[b]), int(at[b + 1])
         if z > a:
             check_prompts(out[a:z], q[a:z], k[a:z], v[a:z], [z - a], 1, 2, causal)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,H,G", [([255, 256, 257], 16, 2), ([1000], 16, 4), ([130, 61, 400], 16, 3),
+                                      ([300, 17, 0, 5], 16, 8), ([90, 200], 16, 5), ([40, 70], 4, 71),
+                                      ([30, 5], 8, 128), ([2500, 700], 4, 4), ([700], 48, 1)])
+def test_prompts_of_many_heads(cuda_lib, lens, H, G, causal, dtype):
+    """Enough work for jobs of two row tiles that share their key tiles (the
+    cases of few heads take jobs of one row tile)."""
+    ctx = context(cuda_lib, H)
+    q, k, v, cu = draw(len(lens) + G, lens, H, G, dtype, 7)
+    k[sum(lens):], v[sum(lens):], q[sum(lens):] = float("nan"), float("inf"), float("nan")
+    out = torch.full_like(q, 5.0)
+    before = out.clone()
+    cuda_lib.isoquant_prompt_attend(ctx, q, k, v, cu, out, causal=causal)
+    torch.cuda.synchronize()
+    assert cuda_lib.isoquant_get_status(ctx) == 0
+    check_prompts(out, q, k, v, lens, H, G, causal, before=before)
+
+
+@pytest.mark.parametrize("rate", [0.002, 0.02, 0.2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_growing_maxima_of_many_heads(cuda_lib, dtype, rate):
+    ctx = context(cuda_lib, 32)
+    q, k, v, cu = draw(9, [1500], 32, 1, dtype)
+    q[..., 0], k[..., 0] = 8.0, (torch.arange(1500, device="cuda") * rate)[:, None].to(k.dtype)
+    out = torch.zeros_like(q)
+    cuda_lib.isoquant_prompt_attend(ctx, q, k, v, cu, out)
+    torch.cuda.synchronize()
+    check_prompts(out, q, k, v, [1500], 32, 1, True)
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_prompt_values_of_many_heads_that_only_later_tokens_see(cuda_lib, dtype, G):
+    """As above in jobs of two row tiles, one head's values alone bad."""
+    csd = cuda_lib
+    H = 64
+    ctx = context(csd, H)
+    lens = [50, 400, 30]
+    q, k, v, cu = draw(61, lens, H, G, dtype)
+    clean = torch.zeros_like(q)
+    csd.isoquant_prompt_attend(ctx, q, k, v, cu, clean)
+    want = clean.clone().float()
+    for t, h, d, x in ((53, 3, 5, float("inf")), (180, 3, 70, float("-inf")), (305, 40, 127, float("nan")),
+                       (449, 63, 0, float("inf"))):
+        v[t, h, d] = x
+        want[t:450, h * G:(h + 1) * G, d] = x
+    out = torch.zeros_like(q)
+    csd.isoquant_prompt_attend(ctx, q, k, v, cu, out)
+    torch.cuda.synchronize()
+    same = torch.isfinite(want)
+    assert torch.equal(out[same], clean[same])
+    assert torch.equal(torch.nan_to_num(out.float()[~same], nan=7.0, posinf=8.0, neginf=9.0),
+                       torch.nan_to_num(want[~same], nan=7.0, posinf=8.0, neginf=9.0))
