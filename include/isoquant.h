@@ -303,7 +303,9 @@ int isoquant_dense_prep(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
                         const int64_t *q_pos, const isoquant_rope *rope,
                         void *k_out, void *q_out, void *stream);
 
-/* Workspace bytes isoquant_dense_attend needs. */
+/* Workspace bytes isoquant_dense_attend needs: two fp32 records per SM of a
+ * row tile's rows (nq tokens times the group's heads, up to 128), whatever the
+ * batch and the lengths. */
 int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq,
                                   int num_q_heads, size_t *bytes);
 
@@ -349,7 +351,8 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
  *      aligned, apart from the inputs; rows of no sequence are left as they
  *      were (a row whose every score is -inf outputs zeros)
  * Scores, softmax statistics and sums in fp32; softmax weights are rounded
- * to `dtype` for the product with v.  One kernel launch, no workspace.
+ * to `dtype` for the product with v.  NaN and infinite values reach the rows
+ * that see their token, no others.  One kernel launch, no workspace.
  * num_q_heads / num_kv_heads at most 128.  Errors: INVALID_ARG, UNSUPPORTED
  * (dtype, group size), ALIGNMENT, CUDA. */
 int isoquant_prompt_attend(isoquant_ctx *ctx, const void *q, const void *k,
