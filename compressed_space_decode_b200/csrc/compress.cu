@@ -88,10 +88,9 @@ struct RopeArgs {
   int rot, inter;
 };
 
-// Four coordinates 4 lane .. 4 lane + 3 of a warp's vector, in the
-// arithmetic of X (float, or double with exact products of fp32 values).
-template <typename X>
-__device__ __forceinline__ void rope4(const RopeArgs &r, int64_t pos, int lane, const float (&x)[4], X (&y)[4]) {
+// Four coordinates 4 lane .. 4 lane + 3 of a warp's vector, in fp64 (products
+// of fp32 values are exact).
+__device__ __forceinline__ void rope4(const RopeArgs &r, int64_t pos, int lane, const float (&x)[4], double (&y)[4]) {
   const float *row = r.table + pos * r.rot;
   const int half = r.rot >> 1, j = 4 * lane;
   if (r.inter) {
@@ -100,9 +99,9 @@ __device__ __forceinline__ void rope4(const RopeArgs &r, int64_t pos, int lane, 
     if (j < r.rot) {
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const X c = row[(j + i) >> 1], s = row[half + ((j + i) >> 1)];
-        y[i] = fma(X(x[i]), c, -(X(x[i + 1]) * s));
-        y[i + 1] = fma(X(x[i + 1]), c, X(x[i]) * s);
+        const double c = row[(j + i) >> 1], s = row[half + ((j + i) >> 1)];
+        y[i] = fma(double(x[i]), c, -(double(x[i + 1]) * s));
+        y[i + 1] = fma(double(x[i + 1]), c, double(x[i]) * s);
       }
     }
     return;
@@ -113,10 +112,10 @@ __device__ __forceinline__ void rope4(const RopeArgs &r, int64_t pos, int lane, 
   const int base = !rotates ? 0 : lower ? j : j - half;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const X o = __shfl_sync(0xffffffffu, x[i], partner);
-    const X c = row[base + i], s = row[half + base + i];
-    const X t = lower ? -(o * s) : o * s;
-    y[i] = rotates ? fma(X(x[i]), c, t) : X(x[i]);
+    const double o = __shfl_sync(0xffffffffu, x[i], partner);
+    const double c = row[base + i], s = row[half + base + i];
+    const double t = lower ? -(o * s) : o * s;
+    y[i] = rotates ? fma(double(x[i]), c, t) : double(x[i]);
   }
 }
 
