@@ -88,7 +88,7 @@ template <typename T, int HC>
 __global__ void __launch_bounds__(256) k_dense_prep(const DensePrepArgs g) {
   pdl_trigger();
   pdl_wait();
-  uint32_t item = (blockIdx.x * 256u + threadIdx.x) >> 3;
+  uint32_t item = blockIdx.x * 32u + (threadIdx.x >> 3);
   const int l8 = threadIdx.x & 7;
   int kind = 0;  // 0: queries, 1: keys, 2: values
   if (item >= g.q_items) {
