@@ -67,8 +67,8 @@ constexpr int kThreads16 = 3 * 128;         // k_attend16: two sides
 // shared memory behind the tiles
 constexpr int kOffBad = 0;                      // first token with +inf, -inf, NaN of each dim
 constexpr int kOffBar = kOffBad + 3 * kD * 4;   // barriers
-constexpr int kOffFlags = kOffBar + 320;
-constexpr int kOffLoc = kOffFlags + 16;         // cache: the CTA's part, then locate's scratch; prompts: two jobs
+constexpr int kOffFlags = kOffBar + 304;
+constexpr int kOffLoc = kOffFlags + 48;         // cache: the CTA's part, then locate's scratch; prompts: two jobs
 constexpr int kTailBytes = kOffLoc + 160;
 constexpr int kOffMl = kTailBytes;              // k_attend16: side 1's (reference, sum) of each row
 
@@ -568,7 +568,7 @@ struct Bars {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
-static_assert(sizeof(Bars) <= 320, "room for the barriers");
+static_assert(sizeof(Bars) <= 304, "room for the barriers");
 // A prompt's piece of work as the loader hands it to the other warps.
 struct Job {
   int kv0, rows, row0, h, n0, n1, end, pad;
@@ -578,8 +578,13 @@ struct Flags {
   uint32_t tmem;
   int abort;
   int nonfinite;  // the segment, counted from 1, that the guard's marks belong to
-  int done;       // softmax warps' ends of segments
+  // Segments behind each reader of the marks: a softmax warp of k_attend16, a
+  // side of k_cols16.  Each has a count of its own: readers are up to two
+  // segments apart (one without tiles of a segment passes it at once), so a
+  // sum would let one stand for another.
+  int done[8];
 };
+static_assert(sizeof(Flags) <= 48, "room for the flags");
 
 // The ring: tile t's keys lie in slot t mod kKeySlots, its values in one of the
 // other slots in turn.  use: how often the slot was used before.
@@ -605,7 +610,8 @@ __device__ __forceinline__ void start_cta(Bars &bars, Flags *flags, int *bad, in
   }
   if (threadIdx.x == 32) {
     bars.init(slot_users, q_users, p_count, seg_count, readers);
-    flags->abort = flags->nonfinite = flags->done = 0;
+    flags->abort = flags->nonfinite = 0;
+    for (int i = 0; i < 8; ++i) flags->done[i] = 0;
   }
   for (int i = threadIdx.x; i < 3 * kD; i += blockDim.x) bad[i] = INT_MAX;
 }
@@ -729,11 +735,11 @@ __device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensor
 
 // The guard warp on a value tile (tokens from t0 on) of segment k: rows that
 // no query row sees are cleared, non-finite elements of rows that some see
-// are taken out and their first token noted for this segment.  per_segment:
-// softmax warps that end each segment.
+// are taken out and their first token noted for this segment.  readers: bit i
+// set if done[i] counts a reader of the marks.  false: gave up waiting.
 template <typename T>
-__device__ __forceinline__ void guard_tile(const Attend16 &p, uint8_t *tile, int t0, int all, int none, int k,
-                                           int per_segment, int *bad, Flags *flags) {
+__device__ __forceinline__ bool guard_tile(const Attend16 &p, uint8_t *tile, int t0, int all, int none, int k,
+                                           uint32_t readers, int *bad, Flags *flags) {
   const uint32_t mask = exponent_mask<T>();
   const int lane = threadIdx.x & 31;
   auto at = [&](int r) {  // this lane's 16 bytes of row r
@@ -753,14 +759,20 @@ __device__ __forceinline__ void guard_tile(const Attend16 &p, uint8_t *tile, int
         any |= (w[i] & mask & 0xffffu) == (mask & 0xffffu) || (w[i] & mask & 0xffff0000u) == (mask & 0xffff0000u);
     }
   }
-  if (!__any_sync(0xffffffffu, any)) return;
+  if (!__any_sync(0xffffffffu, any)) return true;
   // rare: an earlier segment's marks must have been read before they go
-  volatile int *marked = &flags->nonfinite, *done = &flags->done, *abort = &flags->abort;
+  volatile int *marked = &flags->nonfinite, *done = flags->done, *abort = &flags->abort;
   const int before = *marked;
   if (before != k + 1) {
+    const bool reader = (readers >> lane) & 1u;
     const uint64_t start = global_ns();
-    while (*done < before * per_segment && !*abort && global_ns() - start < kWaitLimitNs) __nanosleep(200);
-    if (*done < before * per_segment) set_status(p.status, ISOQUANT_DEVERR_WAIT_TIMEOUT);
+    while (!__all_sync(0xffffffffu, !reader || done[lane] >= before)) {
+      const bool late = global_ns() - start >= kWaitLimitNs;
+      if (late) set_status(p.status, ISOQUANT_DEVERR_WAIT_TIMEOUT);
+      if (late) *abort = 1;
+      if (__any_sync(0xffffffffu, *abort != 0)) return false;
+      __nanosleep(200);
+    }
     for (int e = lane; e < 3 * kD; e += 32) bad[e] = INT_MAX;
     __syncwarp();
   }
@@ -780,17 +792,17 @@ __device__ __forceinline__ void guard_tile(const Attend16 &p, uint8_t *tile, int
   }
   __syncwarp();
   if (lane == 0) *marked = k + 1;
+  return true;
 }
 
 // A loaded tile: seen to, then handed on.  phases: bit i = parity of slot i's loads.
 template <typename T>
 __device__ __forceinline__ bool guard_slot(const Attend16 &p, uint32_t sl, uint32_t &phases, uint8_t *ring_base, int t0,
-                                           int all, int none, int k, int per_segment, int *bad, Bars &bars,
+                                           int all, int none, int k, uint32_t readers, int *bad, Bars &bars,
                                            Flags *flags) {
   const bool ok = warp_wait(&bars.loaded[sl], (phases >> sl) & 1u, p, &flags->abort);
   phases ^= 1u << sl;
-  if (!ok) return false;
-  guard_tile<T>(p, ring_base + sl * kTileBytes, t0, all, none, k, per_segment, bad, flags);
+  if (!ok || !guard_tile<T>(p, ring_base + sl * kTileBytes, t0, all, none, k, readers, bad, flags)) return false;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.full[sl]);
@@ -799,14 +811,14 @@ __device__ __forceinline__ bool guard_slot(const Attend16 &p, uint32_t sl, uint3
 
 // The guard warp over the cache.
 template <typename T>
-__device__ void guard_cache(const Attend16 &p, const int64_t *loc, uint8_t *ring_base, int per_segment, int *bad,
+__device__ void guard_cache(const Attend16 &p, const int64_t *loc, uint8_t *ring_base, uint32_t readers, int *bad,
                             Bars &bars, Flags *flags) {
   uint32_t phases = 0, t = 0;
   cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
     const int all = all_see(p, s), none = none_sees(p, s, p.tok), n = s.n[0];
     bool ok = true;
     for (int i = max(0, all / kTile - s.j0); i < n && ok; ++i)
-      ok = guard_slot<T>(p, value_slot(t + i, p.slots), phases, ring_base, (s.j0 + i) * kTile, all, none, k, per_segment,
+      ok = guard_slot<T>(p, value_slot(t + i, p.slots), phases, ring_base, (s.j0 + i) * kTile, all, none, k, readers,
                          bad, bars, flags);
     t += n;
     return ok;
@@ -1057,16 +1069,18 @@ __global__ void __launch_bounds__(kThreads16, 1)
     }
   } else if (warp == kGuardWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // who reads the marks: side 0, which merges the sides, or both
+    const uint32_t side = (1u << row_warps) - 1u, readers = kAlternate ? side : side | side << 4;
     if constexpr (kPaged) {
-      guard_cache<T>(p, loc, ring_base, row_warps, bad, bars, flags);
+      guard_cache<T>(p, loc, ring_base, readers, bad, bars, flags);
     } else {
       uint32_t phases = 0, t = 0;
       for_segments([&](const Segment &s, uint32_t k) {
         const int all = all_see(p, s), none = none_sees(p, s, p.sides * p.tok), n = tiles(s);
         bool ok = true;
         for (int j = all / kTile; j < n && ok; ++j)
-          ok = guard_slot<T>(p, value_slot(t + j, kRowSlots), phases, ring_base, j * kTile, all, none, k, 2 * row_warps,
-                             bad, bars, flags);
+          ok = guard_slot<T>(p, value_slot(t + j, kRowSlots), phases, ring_base, j * kTile, all, none, k, readers, bad,
+                             bars, flags);
         t += n;
         return ok;
       });
@@ -1088,6 +1102,10 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = with_nonfinite(o[i], bad, col + i, lim);
       }
+    };
+    auto passed = [&](uint32_t k) {  // segment k's marks have been read
+      __syncwarp();
+      if (lane == 0) *const_cast<volatile int *>(&flags->done[warp - 4]) = static_cast<int>(k) + 1;
     };
     auto store16 = [&](T *dst, const float (&o)[32]) {
 #pragma unroll
@@ -1122,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
       const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
       if (!kAlternate) {
         if (n == 0) {
-          if (lane == 0) atomicAdd(&flags->done, 1);
+          passed(k);
           return true;
         }
         ok = warp_wait(&bars.o_done[x], n_o++ & 1u, p, abort);
@@ -1139,15 +1157,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
           if (valid) store16(dst + col, o);
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) atomicAdd(&flags->done, 1);
+        passed(k);
       } else if (x == 1) {
         if (n > 0) ml[r] = make_float2(sub, l);
         __syncwarp();
-        if (lane == 0) {
-          if (n > 0) mbar_arrive(&bars.side1);
-          if (!kPaged) atomicAdd(&flags->done, 1);
-        }
+        if (lane == 0 && n > 0) mbar_arrive(&bars.side1);
       } else {
         const bool both = tiles(s) > 1, whole = !kPaged || s.whole;
         ok = warp_wait(&bars.o_done[0], k & 1u, p, abort);
@@ -1198,11 +1212,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
           }
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars.seg_done);
-          atomicAdd(&flags->done, 1);
-        }
+        passed(k);
+        if (lane == 0) mbar_arrive(&bars.seg_done);
       }
       return true;
     });
@@ -1375,7 +1386,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
   } else if (warp == kLoadWarp) {
     load_cache(p, loc, mq, mk, smem_addr(smem), smem_addr(ring_base), C::kQBufs, bars, abort);
   } else if (warp == kGuardWarp) {
-    guard_cache<T>(p, loc, ring_base, soft_warps, bad, bars, flags);
+    guard_cache<T>(p, loc, ring_base, (1u << soft_warps / 4) - 1u, bad, bars, flags);
   } else {
     // -------------------------------------------------------------- softmax
     const int x = (warp >> 2) - 1, t = tid & (kTile - 1), row0 = x * SR;
@@ -1549,8 +1560,8 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
         }
       }
       tc_fence_before();
-      side_sync(x);  // sums and factors are read
-      if (lane == 0) atomicAdd(&flags->done, 1);
+      side_sync(x);  // sums, factors and marks are read
+      if (t == 0) *const_cast<volatile int *>(&flags->done[x]) = static_cast<int>(k) + 1;
       return true;
     });
   }
