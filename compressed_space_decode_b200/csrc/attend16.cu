@@ -81,6 +81,8 @@ struct Attend16 {
   int n_tok;
   const int32_t *page_table, *seq_lens;             // cache
   int max_pages, num_pages, ps_shift;
+  const uint16_t *values;                           // the cache, or the prompts' V with tokens v_stride apart
+  int64_t v_stride;
   float *records;
   int2 *plan;
   int n_cta, row_stride;                            // records: rows rounded up to 2
@@ -526,15 +528,77 @@ __device__ bool find_prompt(const Attend16 &p, uint32_t job, Segment &s) {
   return true;
 }
 
-// Every wait of a warp: false once it, or any other of the CTA, gave up.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Attend16 &p, volatile int *abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, abort));
-}
-
 // 16-bit patterns whose exponent is all ones
 template <typename T>
 __device__ __forceinline__ uint32_t exponent_mask() {
   return std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
+}
+
+// The non-finite values of a head's tokens [t0, end), all of them in the
+// sequence: lane l has dims 8 (l mod 16) .. + 7, three bits a dim (+inf, -inf,
+// NaN).  The products lose an infinity where its weight, or a bf16 weight's
+// remainder, is zero or negative (0 x inf); a sum that came out NaN looks here
+// what it should be.  Rare, and kept out of line so that it costs the loops
+// nothing; one whole warp.  values: the head's first value vector, of token 0 or
+// page 0; stride: elements from token to token, or page to page.
+template <bool kPaged>
+__device__ __noinline__ uint32_t values_seen(const int32_t *pages, int num_pages, int ps_shift,
+                                             const uint16_t *values, int64_t stride, int t0, int end, uint32_t mask) {
+  const int lane = threadIdx.x & 31;
+  values += 8 * (lane & 15);
+  constexpr int kAtOnce = 8;
+  constexpr uint32_t kNans = 0x924924u;  // a lane's dims all NaN: no token changes that
+  uint32_t kinds = 0;
+  for (int first = t0; first < end && !__all_sync(0xffffffffu, (kinds & kNans) == kNans); first += 2 * kAtOnce) {
+    uint4 v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int t = first + 2 * i + (lane >> 4);
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < end) {
+        int64_t at = t * stride;
+        if constexpr (kPaged) {
+          const int page = pages[t >> ps_shift];
+          at = (page < 0 || page >= num_pages ? 0 : page * stride) + (t & ((1 << ps_shift) - 1)) * kD;
+        }
+        v[i] = *reinterpret_cast<const uint4 *>(values + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+        if ((x & mask) == mask) kinds |= ((x & 0x7fffu) != mask ? 4u : 1u << (x >> 15)) << (3 * e);
+      }
+    }
+    kinds |= __shfl_xor_sync(0xffffffffu, kinds, 16);
+  }
+  return kinds;
+}
+template <typename T, bool kPaged>
+__device__ __forceinline__ uint32_t values_seen(const Attend16 &p, const Segment &s, int t0, int end) {
+  const uint32_t mask = exponent_mask<T>() & 0xffffu;
+  if constexpr (kPaged)
+    return values_seen<true>(p.page_table + static_cast<int64_t>(s.b) * p.max_pages, p.num_pages, p.ps_shift,
+                             p.values + (static_cast<int64_t>(p.H + s.h) << p.ps_shift) * kD,
+                             (static_cast<int64_t>(2 * p.H) << p.ps_shift) * kD, t0, end, mask);
+  else
+    return values_seen<false>(nullptr, 0, 0, p.values + s.kv0 * p.v_stride + static_cast<int64_t>(s.h) * kD,
+                              p.v_stride, t0, end, mask);
+}
+// dim d's three bits of what values_seen returned
+__device__ __forceinline__ uint32_t kinds_of(uint32_t seen, int d) {
+  return (__shfl_sync(0xffffffffu, seen, d >> 3) >> (3 * (d & 7))) & 7u;
+}
+__device__ __forceinline__ float nonfinite_sum(uint32_t kinds) {
+  return kinds == 1u ? INFINITY : kinds == 2u ? -INFINITY : NAN;
+}
+
+// Every wait of a warp: false once it, or any other of the CTA, gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Attend16 &p, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, abort));
 }
 
 // The barriers of a CTA: ring slots filled (for a tile that the guard sees to
@@ -1094,10 +1158,15 @@ __global__ void __launch_bounds__(kThreads16, 1)
     const int r_tok = r / p.GB, r_head = r - r_tok * p.GB;
     uint32_t n_s = 0, n_o1 = 0, n_o = 0;
     bool ok = true;
-    // one row's sum of products, times f, plus what the guards took out
-    auto finish = [&](uint32_t k, int lim, float (&o)[32], int col, float f) {
+    // one row's sum of products, times f, plus what the guards took out; a NaN
+    // of the sum stays in `worst`
+    auto finish = [&](uint32_t k, int lim, float (&o)[32], int col, float f, float &worst) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] *= f;
+      for (int i = 0; i < 32; i += 2) {
+        o[i] *= f;
+        o[i + 1] *= f;
+        worst = max3_nan(worst, o[i], o[i + 1]);
+      }
       if (*nonfinite == static_cast<int>(k) + 1) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = with_nonfinite(o[i], bad, col + i, lim);
@@ -1106,6 +1175,21 @@ __global__ void __launch_bounds__(kThreads16, 1)
     auto passed = [&](uint32_t k) {  // segment k's marks have been read
       __syncwarp();
       if (lane == 0) *const_cast<volatile int *>(&flags->done[warp - 4]) = static_cast<int>(k) + 1;
+    };
+    // Infinities that the products lost, put right where the row was stored
+    // (rare: a loop that takes no room in the code above).  sees: a valid row
+    // whose sum of weights is a number; lim: 0 for a row that is zero.
+    auto repair = [&](const Segment &s, uint32_t k, bool sees, int lim, auto *dst) {
+      const int t0 = s.j0 * kTile, end = min(all_see(p, s), t0 + tiles(s) * kTile);
+      const uint32_t seen = values_seen<T, kPaged>(p, s, t0, end);
+      for (int d = 0; d < kD; ++d) {
+        const uint32_t kinds = kinds_of(seen, d);
+        if (sees && kinds != 0 && isnan(static_cast<float>(dst[d]))) {
+          float y = lim > 0 ? nonfinite_sum(kinds) : 0.f;
+          if (*nonfinite == static_cast<int>(k) + 1) y = with_nonfinite(y, bad, d, lim);
+          dst[d] = y;
+        }
+      }
     };
     auto store16 = [&](T *dst, const float (&o)[32]) {
 #pragma unroll
@@ -1149,13 +1233,17 @@ __global__ void __launch_bounds__(kThreads16, 1)
         const float inv = l != 0.f ? 1.f / l : 0.f;
         T *dst = static_cast<T *>(p.out) +
                  (static_cast<int64_t>(s.kv0 + qi) * p.Hq + static_cast<int64_t>(s.h) * p.G + hq) * kD;
+        const int lim0 = l != 0.f ? lim : 0;  // every score -inf: zero
+        float worst = 0.f;
 #pragma unroll
         for (int col = 0; col < kD; col += 32) {
           float o[32];
           tmem_ld32(to + col, o);
-          finish(k, lim, o, col, inv);
+          finish(k, lim0, o, col, inv, worst);
           if (valid) store16(dst + col, o);
         }
+        const bool sees = valid && l == l;
+        if (__any_sync(0xffffffffu, sees && isnan(worst))) repair(s, k, sees, lim0, dst);
         tc_fence_before();
         passed(k);
       } else if (x == 1) {
@@ -1189,6 +1277,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
         T *dst = static_cast<T *>(p.out) + (row * p.Hq +
                                             static_cast<int64_t>(s.h) * p.G + hq) * kD;
         if (valid && !whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
+        const int lim0 = !whole || l != 0.f ? lim : 0;
+        float worst = 0.f;
 #pragma unroll
         for (int col = 0; col < kD; col += 32) {
           float o[32];
@@ -1199,7 +1289,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
           }
-          finish(k, lim, o, col, whole ? inv : 1.f);
+          finish(k, lim0, o, col, whole ? inv : 1.f, worst);
           if (valid) {
             if (whole) {
               store16(dst + col, o);
@@ -1210,6 +1300,11 @@ __global__ void __launch_bounds__(kThreads16, 1)
                     make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
+        }
+        const bool sees = valid && l == l;
+        if (__any_sync(0xffffffffu, sees && isnan(worst))) {
+          if (whole) repair(s, k, sees, lim0, dst);
+          else repair(s, k, sees, lim0, rec + 2 * p.row_stride + r * kD);
         }
         tc_fence_before();
         passed(k);
@@ -1541,6 +1636,17 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < SR; ++r) o[r] += e[r];
       }
+      // infinities that the products lost
+      bool lost = false;
+#pragma unroll
+      for (int r = 0; r < SR; ++r) lost |= isnan(o[r]);
+      if (__any_sync(0xffffffffu, ok && lost)) {
+        const int t0 = s.j0 * kTile;
+        const uint32_t kinds = kinds_of(values_seen<T, true>(p, s, t0, min(all, t0 + n * kTile)), t);
+#pragma unroll
+        for (int r = 0; r < SR; ++r)
+          if (isnan(o[r]) && kinds != 0) o[r] = nonfinite_sum(kinds);
+      }
       if (ok) {
         int qi = s.row0 + tok0, head = head0;
         T *out = static_cast<T *>(p.out) + (static_cast<int64_t>(s.h) * p.G + s.chunk * kTile) * kD + t;
@@ -1548,8 +1654,9 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < SR; ++r) {
           if (row0 + r < p.R && qi < s.rows && head < heads) {
-            float y = o[r] * factor[r];
-            if (*nonfinite == static_cast<int>(k) + 1) y = with_nonfinite(y, bad, t, s.limit(qi, p.causal));
+            const bool zero = factor[r] == 0.f;  // every score -inf
+            float y = zero ? 0.f : o[r] * factor[r];
+            if (!zero && *nonfinite == static_cast<int>(k) + 1) y = with_nonfinite(y, bad, t, s.limit(qi, p.causal));
             if (s.whole) out[((static_cast<int64_t>(s.b) * p.nq + qi) * p.Hq + head) * kD] = to16(y, T());
             else rec[2 * p.row_stride + (row0 + r) * kD + t] = y;
           }
@@ -1598,6 +1705,9 @@ __global__ void __launch_bounds__(128) k_combine16(const Attend16 p) {
       const float2 t = *reinterpret_cast<const float2 *>(rec(i0 + lane) + 2 * r);
       w = ex2f(t.x - base);
       l += w * t.y;
+      // an infinite sum counts however small its weight: 0 x inf would be NaN
+      // (a NaN weight's sum of weights is NaN too)
+      w = fmaxf(w, __uint_as_float(1u));
     }
     const int top = min(32, count - i0);
 #pragma unroll 8
@@ -1610,6 +1720,7 @@ __global__ void __launch_bounds__(128) k_combine16(const Attend16 p) {
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (l == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);  // every score -inf
   const float inv = l != 0.f ? 1.f / l : 0.f;
   T *dst = static_cast<T *>(p.out) +
            ((static_cast<int64_t>(b) * p.nq + qi) * p.Hq + static_cast<int64_t>(h) * p.G + hq) * kD + 4 * lane;
@@ -1731,6 +1842,8 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   p.n_tok = n_tok;
   p.slots = kRowSlots;
   p.q_half = kTileBytes / 2;
+  p.values = static_cast<const uint16_t *>(v);
+  p.v_stride = v_stride;
   p.out = out;
   p.status = ctx->status;
   p.device = ctx->device;
@@ -1780,6 +1893,7 @@ cudaError_t launch_dense_attend(const isoquant_ctx *ctx, const isoquant_dense_ca
   p.max_pages = max_pages;
   p.num_pages = cache->num_pages;
   while ((1 << p.ps_shift) < cache->page_size) ++p.ps_shift;
+  p.values = static_cast<const uint16_t *>(cache->data);
   p.n_cta = ctx->num_sms;
   p.plan = static_cast<int2 *>(ws);
   p.records = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(p.n_cta));

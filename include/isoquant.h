@@ -322,7 +322,9 @@ int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq,
  *        aligned; its contents on entry do not matter; calls whose kernels
  *        overlap on the GPU must not share one workspace
  * A row that sees no token, or only keys whose scores are -inf, outputs
- * zeros; a NaN score makes its row NaN.  A length beyond the page table's
+ * zeros; a NaN score makes its row NaN.  An infinite value makes its element
+ * infinite in the rows that see its token, however small the weight; both
+ * signs, or a NaN, make it NaN.  A length beyond the page table's
  * max_pages pages sets ISOQUANT_DEVERR_PAGE_RANGE and counts as their tokens.
  * Two kernel launches.  Errors: INVALID_ARG (also more than 2^31 - 1 cached
  * vectors), UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
@@ -352,7 +354,7 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
  *      were (a row whose every score is -inf outputs zeros)
  * Scores, softmax statistics and sums in fp32; softmax weights are rounded
  * to `dtype` for the product with v.  NaN and infinite values reach the rows
- * that see their token, no others.  One kernel launch, no workspace.
+ * that see their token, no others, as in isoquant_dense_attend.  One kernel launch, no workspace.
  * num_q_heads / num_kv_heads at most 128.  Errors: INVALID_ARG, UNSUPPORTED
  * (dtype, group size), ALIGNMENT, CUDA. */
 int isoquant_prompt_attend(isoquant_ctx *ctx, const void *q, const void *k,
