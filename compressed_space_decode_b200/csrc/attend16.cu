@@ -47,6 +47,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -211,15 +212,21 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
 // The reference passed by 2^kLazy moves; fp16 weights are held times 2^7 so
 // that those far below the maximum keep their bits (2^15 at most).
 constexpr float kLazy = 8.f;
+// The reference is kept as the score itself: c s - (c times reference rounded)
+// is off by that rounding, up to 2^9 for logarithms of 2^33.  It scales a row's
+// weights alike, so it cancels while it fits the exponents; from here on the
+// difference of the scores is taken first.
+constexpr float kLarge = 1048576.f;  // rounded within 2^-4
 template <typename T>
 constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 // One key tile of a softmax thread's row: scores at tensor-memory columns ts,
-// of which the first `vis` count, become weights 2^(c s - sub) at the same
+// of which the first `vis` count, become weights 2^(c (s - ref)) at the same
 // columns; with kLo the weights' remainders follow as a second operand.
+// any_large: whether a row of the warp has a large reference.
 template <typename T, bool kLo>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int vis, bool first, float &ref,
-                                             float &l) {
+                                             float &l, bool &any_large) {
   constexpr float kMost = kShift<T> == 0.f ? 256.f : 32768.f;  // 2^(8 + shift)
   const float2 c2 = make_float2(c, c);
   float sum;
@@ -243,10 +250,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) mx[j] = max3_nan(mx[j], s[i >> 5][(i + j) & 31], s[i >> 5][(i + j + 4) & 31]);
       }
-      const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * c;
+      const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
       const bool up = move && !(mt <= ref);
-      const float corr = up ? ex2f(ref - mt) : 1.f;
+      const float corr = up ? ex2f((ref - mt) * c) : 1.f;
       if (up) ref = mt;
+      any_large = __any_sync(0xffffffffu, fabsf(ref * c) > kLarge && ref != -INFINITY);
       l *= corr;
       if (!first) {
 #pragma unroll
@@ -260,7 +268,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
       }
     }
     // (NaN for a NaN or +inf)
-    const float sub = ref == -INFINITY ? 0.f : (ref - kShift<T>) + (ref - ref);
+    float sub = ref == -INFINITY ? 0.f : (ref * c - kShift<T>) + (ref - ref);
+    if (any_large) {
+      const float off = ref == -INFINITY ? 0.f : -ref;
+      sub = -kShift<T>;
+#pragma unroll
+      for (int i = 0; i < kTile; i += 2) {
+        const float2 v = __fadd2_rn(make_float2(s[i >> 5][i & 31], s[i >> 5][(i & 31) + 1]), make_float2(off, off));
+        s[i >> 5][i & 31] = v.x;
+        s[i >> 5][(i & 31) + 1] = v.y;
+      }
+    }
     const float2 n2 = make_float2(-sub, -sub);
     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1205,6 +1223,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
       const bool valid = r < p.R && qi < s.rows && hq < p.G;
       const int lim = valid ? s.limit(qi, p.causal) : 0;
       float ref = -INFINITY, l = 0.f;
+      bool any_large = false;
       for (int i = 0; i < n && ok; ++i) {
         const int t0 = (s.j0 + (kAlternate ? 2 * i + x : i)) * kTile;
         ok = warp_wait(&bars.s_full[x], n_s & 1u, p, abort);
@@ -1215,13 +1234,13 @@ __global__ void __launch_bounds__(kThreads16, 1)
         if (kAlternate && x == 1 && k > 0 && i == 0) ok = ok && warp_wait(&bars.seg_done, (k - 1) & 1u, p, abort);
         if (!ok) break;
         tc_fence_after();
-        softmax_tile<T, kLo>(ts, to, p.c, lim - t0, i == 0, ref, l);
+        softmax_tile<T, kLo>(ts, to, p.c, lim - t0, i == 0, ref, l, any_large);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[x]);
       }
       if (!ok) return false;
-      const float sub = ref == -INFINITY ? -INFINITY : ref - kShift<T>;
+      const float sub = ref * p.c - kShift<T>;  // (-inf if it saw nothing)
       if (!kAlternate) {
         if (n == 0) {
           passed(k);
@@ -1350,14 +1369,16 @@ struct Cols {
   static constexpr int kRing = kP + kPBufs * kPBytes;
   static constexpr int kTail = kRing + kSlots * kTileBytes;
   // Each row's reference, the score above which it moves, what is added to a
-  // score's logarithm, what an O column is multiplied by, and four warps'
-  // maxima or sums.
+  // score's logarithm, what an O column is multiplied by, four warps' maxima
+  // or sums, and what is taken from large scores.
   static constexpr int kRefs = kTail + kTailBytes + 64;  // (locate's scratch: a word of 8 bytes per warp)
   static constexpr int kLimits = kRefs + NR * 4;
   static constexpr int kSubs = kLimits + NR * 4;
   static constexpr int kFactor = kSubs + NR * 4;
   static constexpr int kPart = kFactor + NR * 4;
-  static constexpr int kBytes = kPart + 4 * NR * 4;
+  static constexpr int kOff = kPart + 4 * NR * 4;
+  static constexpr int kAnyOff = kOff + NR * 4;    // whether a side has such a row
+  static constexpr int kBytes = kAnyOff + 16;
   static constexpr uint32_t kColO = 2 * NR;            // S^T buffers at 0 and NR
   static constexpr uint32_t kCols = kColO + kN <= 64 ? 64 : kColO + kN <= 128 ? 128 : 256;
   static_assert(kRing % 1024 == 0 && kBytes <= 227 * 1024 && kColO + kN <= kCols, "layout");
@@ -1492,6 +1513,9 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
     float *subs = reinterpret_cast<float *>(smem + C::kSubs) + row0;
     float *factor = reinterpret_cast<float *>(smem + C::kFactor) + row0;
     float *part = reinterpret_cast<float *>(smem + C::kPart) + 4 * row0;
+    float *offs = reinterpret_cast<float *>(smem + C::kOff) + row0;
+    int *any_off = reinterpret_cast<int *>(smem + C::kAnyOff) + x;
+    bool large_rows = false;  // *any_off
     const int tok0 = row0 / p.GB, head0 = row0 - tok0 * p.GB;
     uint32_t n_s = 0;  // tiles so far
     bool ok = true;
@@ -1545,17 +1569,22 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
           side_sync(x);
           if (t < SR) {
             const float m = max3_nan(max3_nan(part[t], part[SR + t], part[2 * SR + t]), part[3 * SR + t],
-                                     part[3 * SR + t]) * p.c;
+                                     part[3 * SR + t]);
             const float old = i == 0 ? -INFINITY : refs[t];
-            const bool up = !(m <= old + kLazy);
+            const float lazy = fminf(kLazy / p.c, FLT_MAX);
+            const bool up = !(m <= old + lazy);
             const float ref = up ? m : old;
-            factor[t] = up ? ex2f(old - m) : 1.f;
+            factor[t] = up ? ex2f((old - m) * p.c) : 1.f;
             refs[t] = ref;
-            // (a reference of +inf keeps its limit at +inf: only a NaN is above)
-            limits[t] = ref == INFINITY ? INFINITY : (ref + kLazy) / p.c;
-            subs[t] = ref == -INFINITY ? 0.f : kShift<T> - ref;
+            limits[t] = ref + lazy;  // (+inf stays: only a NaN is above)
+            const bool large = fabsf(ref * p.c) > kLarge && ref != -INFINITY;
+            offs[t] = large ? ref : 0.f;
+            subs[t] = ref == -INFINITY ? 0.f : large ? kShift<T> : kShift<T> - ref * p.c;
+            const bool any = __any_sync((1u << SR) - 1u, large);
+            if (t == 0) *any_off = any;
           }
           side_sync(x);
+          large_rows = *any_off != 0;
           if (i > 0) {
             // the last product must be done
             ok = ok && product(n_s - 1);
@@ -1573,6 +1602,10 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
             }
             tmem_stored();
           }
+        }
+        if (large_rows) {
+#pragma unroll
+          for (int r = 0; r < SR; ++r) v[r] -= offs[r];
         }
         uint32_t w[SR / 2], e[SR / 2];  // weights and their remainders, two rows each
 #pragma unroll
@@ -1622,20 +1655,23 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
         factor[t] = !s.whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
         if (!s.whole && row0 + t < p.R)
           *reinterpret_cast<float2 *>(rec + 2 * (row0 + t)) =
-              make_float2(refs[t] - kShift<T>, sum);
+              make_float2(refs[t] * p.c - kShift<T>, sum);
       }
       ok = ok && product(n_s - 1);
       tc_fence_after();
       side_sync(x);
       // thread t: dim t of the side's rows
       float o[SR];
-      tmem_ld_cols<SR>(to, o);
-      if constexpr (kLo) {
-        float e[SR];
-        tmem_ld_cols<SR>(to + NR, e);
+      auto load_o = [&]() {
+        tmem_ld_cols<SR>(to, o);
+        if constexpr (kLo) {
+          float e[SR];
+          tmem_ld_cols<SR>(to + NR, e);
 #pragma unroll
-        for (int r = 0; r < SR; ++r) o[r] += e[r];
-      }
+          for (int r = 0; r < SR; ++r) o[r] += e[r];
+        }
+      };
+      load_o();
       // infinities that the products lost
       bool lost = false;
 #pragma unroll
@@ -1643,6 +1679,7 @@ __global__ void __launch_bounds__(Cols<T, NR>::kThreads, 1)
       if (__any_sync(0xffffffffu, ok && lost)) {
         const int t0 = s.j0 * kTile;
         const uint32_t kinds = kinds_of(values_seen<T, true>(p, s, t0, min(all, t0 + n * kTile)), t);
+        load_o();  // (rather than kept across the call)
 #pragma unroll
         for (int r = 0; r < SR; ++r)
           if (isnan(o[r]) && kinds != 0) o[r] = nonfinite_sum(kinds);
