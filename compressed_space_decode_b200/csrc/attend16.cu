@@ -733,6 +733,7 @@ struct Loader {
   // lane i: slot i's uses, those that the guard sees to, and whether the last was one
   uint32_t uses = 0, guards = 0;
   bool guarded = false;
+  uint32_t queries = 0;  // lane i: loads into query buffer i
   __device__ Loader(const Attend16 &p_, Bars &b, volatile int *a) : p(p_), bars(b), abort(a) {}
   __device__ uint64_t *begin(uint32_t slot, uint32_t use, bool guard, uint32_t bytes) {
     if (use > 0) ok = ok && warp_wait(&bars.freed[slot], (use - 1) & 1u, p, abort);
@@ -748,10 +749,21 @@ struct Loader {
     __syncwarp();
     return bar;
   }
-  // before a CTA that gave up ends: waits for the copies
+  // Waits until query buffer qb, used `use` times before, is free: true for the
+  // lane that loads it (box after box on bars.q_full[qb]).
+  __device__ bool begin_queries(uint32_t qb, uint32_t use) {
+    if (use > 0) ok = ok && warp_wait(&bars.q_free[qb], (use - 1) & 1u, p, abort);
+    const uint32_t lane = threadIdx.x & 31;
+    if (ok && lane == qb) ++queries;
+    if (ok && lane == 0) mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(p.R * kD * 2));
+    return ok && lane == 0;
+  }
+  // The last copies have landed before the CTA ends, whoever of it gave up (else
+  // those that use them wait for them anyway).
   __device__ void drain() {
     const uint32_t lane = threadIdx.x & 31, n = guarded ? guards : uses;
-    if (!ok && n > 0) mbar_wait(guarded ? &bars.loaded[lane] : &bars.full[lane], (n - 1) & 1u, p.status, nullptr);
+    if (n > 0) mbar_wait(guarded ? &bars.loaded[lane] : &bars.full[lane], (n - 1) & 1u, p.status, nullptr);
+    if (queries > 0) mbar_wait(&bars.q_full[lane], (queries - 1) & 1u, p.status, nullptr);
     __syncwarp();
   }
 };
@@ -767,10 +779,8 @@ __device__ void load_cache(const Attend16 &p, const int64_t *loc, const CUtensor
   Loader ld(p, bars, abort);
   uint32_t t = 0;  // tiles so far
   cache_segments(p, loc, [&](const Segment &s, uint32_t k) {
-    const uint32_t qb = k % q_bufs, use = k / q_bufs;
-    if (use > 0) ld.ok = ld.ok && warp_wait(&bars.q_free[qb], (use - 1) & 1u, p, abort);
-    if (lane == 0 && ld.ok) {
-      mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(p.R * kD * 2));
+    const uint32_t qb = k % q_bufs;
+    if (ld.begin_queries(qb, k / q_bufs)) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
         tma_3d(sq + (2 * qb + hf) * p.q_half, &mq, 64 * hf, s.h * p.G + s.chunk * kTile, s.b * p.nq + s.row0,
@@ -1111,10 +1121,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
         auto load_q = [&](int x) {
           if (s.n[x] == 0) return;
           uint32_t &n_q = x ? n_q1 : n_q0;
-          if (n_q > 0) ld.ok = ld.ok && warp_wait(&bars.q_free[x], (n_q - 1) & 1u, p, abort);
-          ++n_q;
-          if (lane == 0 && ld.ok) {
-            mbar_arrive_expect_tx(&bars.q_full[x], static_cast<uint32_t>(p.R * kD * 2));
+          if (ld.begin_queries(x, n_q++)) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
               tma_3d(sq + (2 * x + hf) * p.q_half, &mq, 64 * hf, s.h * p.G, s.kv0 + s.row0 + (kAlternate ? 0 : x * p.tok),
