@@ -313,6 +313,14 @@ def _positions(t, n):
     assert t.dtype is torch.int64 and t.shape == (n,) and t.is_contiguous()
 
 
+def _fits(ctx, cache):
+    """The kernels address a packed cache by the context's heads and code width."""
+    shape = (cache.num_pages, 2, ctx.num_kv_heads, WORDS_FOR[ctx.bits], cache.page_size)
+    codes, norms = cache.codes, cache.norms
+    assert codes.shape == shape and norms.shape == shape[:3] + shape[4:]
+    assert codes.is_contiguous() and norms.is_contiguous()
+
+
 def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_rot, stream=None):
     """isoquant_decode_prep with keys rotated to positions k_pos (int64
     [n_tok]) before they are compressed and query rows to q_pos (int64
@@ -324,6 +332,7 @@ def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, r
     _positions(slot_mapping, n)
     _positions(k_pos, n)
     _positions(q_pos, rows)
+    _fits(ctx, cache)
     status = lib().isoquant_decode_prep_rope(ctx.handle, cache.c_struct(), k.data_ptr(), v.data_ptr(), n,
                                              slot_mapping.data_ptr(), k_pos.data_ptr(), q.data_ptr(), _dtype(q), rows,
                                              q.shape[1], q_pos.data_ptr(), rope.c_struct(), q_rot.data_ptr(),

@@ -1,0 +1,72 @@
+"""What the Python calls of the rotated appends and the 16-bit attention refuse
+before they hand addresses over, on the host: the library's functions are
+stood in for by one that counts its calls."""
+import pytest
+import torch
+
+import compressed_space_decode_b200 as native
+
+BF = torch.bfloat16
+
+
+class Library:
+    """Every function succeeds and is noted."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+class Ctx:
+    handle, num_kv_heads, bits, device = None, 2, 3, -1  # the device index of host tensors
+
+
+
+@pytest.fixture
+def library(monkeypatch):
+    stand_in = Library()
+    monkeypatch.setattr(native, "lib", lambda: stand_in)
+    return stand_in
+
+
+def packed(pages=2, heads=2, words=13, ps=64, **other):
+    shape = {"codes": (pages, 2, heads, words, ps), "norms": (pages, 2, heads, ps)}
+    shape.update(other)
+    return native.PagedCache(torch.zeros(shape["codes"], dtype=torch.int32),
+                             torch.zeros(shape["norms"], dtype=torch.float16), ps)
+
+
+def append(cache, ctx=Ctx(), **changed):
+    k, q = torch.zeros(5, ctx.num_kv_heads, 128, dtype=BF), torch.zeros(5, 8, 128, dtype=BF)
+    pos = torch.zeros(5, dtype=torch.int64)
+    args = dict(k=k, v=k, slot_mapping=pos, k_pos=pos, q=q, q_pos=pos, rope=native.Rope(torch.zeros(9, 128)),
+                q_rot=torch.zeros(5, 8, 128))
+    args.update(changed)
+    native.isoquant_decode_prep_rope(ctx, cache, stream=0, **args)
+
+
+def test_packed_cache_has_to_fit_the_context(library):
+    append(packed())
+    assert [name for name, _ in library.calls] == ["isoquant_decode_prep_rope"]
+    wide = packed()
+    wide.codes = torch.zeros((2, 2, 2, 13, 128), dtype=torch.int32)[..., ::2]
+    late = packed()
+    late.page_size = 128
+    short = packed()
+    short.num_pages = 3
+    for cache in (packed(heads=1), packed(heads=3), packed(words=8), packed(words=16),
+                  packed(codes=(2, 2, 2, 13, 32)), packed(norms=(2, 2, 1, 64)),
+                  packed(norms=(1, 2, 2, 64)), packed(norms=(2, 2, 2, 32)), wide, late, short):
+        with pytest.raises(AssertionError):
+            append(cache)
+    four = Ctx()
+    four.bits = 4
+    with pytest.raises(AssertionError):
+        append(packed(), four)
+    append(packed(words=16), four)
+    assert len(library.calls) == 2
