@@ -310,7 +310,7 @@ def _address(t):
 
 
 def _positions(t, n):
-    assert t.dtype is torch.int64 and t.shape == (n,) and t.is_contiguous()
+    assert t is not None and t.dtype is torch.int64 and t.shape == (n,) and t.is_contiguous()
 
 
 def _fits(ctx, cache):
@@ -353,7 +353,7 @@ def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q
     assert q.shape == q_out.shape == (rows, q.shape[1], HEAD_DIM) and q.is_contiguous() and q_out.is_contiguous()
     assert q.dtype is dtype and q_out.dtype is dtype
     if cache is not None:
-        assert v.shape == k.shape and v.is_contiguous() and v.dtype is dtype
+        assert v is not None and v.shape == k.shape and v.is_contiguous() and v.dtype is dtype
         assert cache.num_kv_heads == ctx.num_kv_heads
         _positions(slot_mapping, n)
     if rope is not None:

@@ -70,3 +70,30 @@ def test_packed_cache_has_to_fit_the_context(library):
         append(packed(), four)
     append(packed(words=16), four)
     assert len(library.calls) == 2
+
+
+def dense(pages=2, ps=64, dtype=BF):
+    return native.DenseCache(torch.zeros((pages, 2, 2, ps, 128), dtype=dtype), ps)
+
+
+def dense_append(**changed):
+    k, q = torch.zeros(5, 2, 128, dtype=BF), torch.zeros(5, 8, 128, dtype=BF)
+    pos = torch.zeros(5, dtype=torch.int64)
+    args = dict(ctx=Ctx(), cache=dense(), k=k, v=k, slot_mapping=pos, k_pos=pos, q=q, q_pos=pos,
+                rope=native.Rope(torch.zeros(9, 128)), q_out=q)
+    args.update(changed)
+    native.isoquant_dense_prep(stream=0, **args)
+
+
+def test_missing_tensors(library):
+    for missing in ("slot_mapping", "k_pos", "q_pos"):
+        with pytest.raises(AssertionError):
+            append(packed(), **{missing: None})
+    for missing in ("v", "slot_mapping", "k_pos", "q_pos"):
+        with pytest.raises(AssertionError):
+            dense_append(**{missing: None})
+    assert library.calls == []
+    # what a call without rotation, or without a cache, does not look at
+    dense_append(rope=None, k_pos=None, q_pos=None)
+    dense_append(cache=None, v=None, slot_mapping=None, k_out=torch.zeros(5, 2, 128, dtype=BF))
+    assert len(library.calls) == 2
