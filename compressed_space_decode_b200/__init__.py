@@ -198,13 +198,21 @@ class DenseCache:
     [pages][2 (K,V)][H][page_size][128]."""
 
     def __init__(self, data, page_size):
-        assert data.dtype in (torch.bfloat16, torch.float16) and data.is_contiguous()
-        assert data.dim() == 5 and data.shape[1] == 2 and data.shape[3] == page_size and data.shape[4] == HEAD_DIM
+        self.page_size = page_size
         self.data = data
+
+    @property
+    def data(self):
+        return self._data
+
+    @data.setter
+    def data(self, data):
+        assert data.dtype in (torch.bfloat16, torch.float16) and data.is_contiguous()
+        assert data.dim() == 5 and data.shape[1] == 2 and data.shape[3] == self.page_size and data.shape[4] == HEAD_DIM
+        self._data = data
         self.num_kv_heads = data.shape[2]
         self.num_pages = data.shape[0]
-        self.page_size = page_size
-        self._c = _DenseCache(data.data_ptr(), _dtype(data), self.num_pages, page_size)
+        self._c = _DenseCache(data.data_ptr(), _dtype(data), self.num_pages, self.page_size)
 
     @staticmethod
     def allocate(num_kv_heads, num_pages, page_size, dtype=torch.bfloat16, device="cuda"):
@@ -212,6 +220,7 @@ class DenseCache:
                           page_size)
 
     def c_struct(self):
+        self._c.data = self._data.data_ptr()  # (its storage may have been replaced in place)
         return self._c
 
 
@@ -221,12 +230,20 @@ class Rope:
     pair up: (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved."""
 
     def __init__(self, cos_sin, rot_dim=HEAD_DIM, interleaved=False):
-        assert cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
-        assert cos_sin.dim() == 2 and cos_sin.shape[1] == rot_dim
-        self.cos_sin = cos_sin
         self.rot_dim = rot_dim
         self.interleaved = bool(interleaved)
-        self._c = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], rot_dim, int(self.interleaved))
+        self.cos_sin = cos_sin
+
+    @property
+    def cos_sin(self):
+        return self._cos_sin
+
+    @cos_sin.setter
+    def cos_sin(self, cos_sin):
+        assert cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
+        assert cos_sin.dim() == 2 and cos_sin.shape[1] == self.rot_dim
+        self._cos_sin = cos_sin
+        self._c = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], self.rot_dim, int(self.interleaved))
 
     @staticmethod
     def table(num_positions, rot_dim=HEAD_DIM, base=10000.0, device="cuda"):
@@ -236,6 +253,7 @@ class Rope:
         return torch.cat([ang.cos(), ang.sin()], 1).float()
 
     def c_struct(self):
+        self._c.cos_sin = self._cos_sin.data_ptr()
         return self._c
 
 

@@ -97,3 +97,32 @@ def test_missing_tensors(library):
     dense_append(rope=None, k_pos=None, q_pos=None)
     dense_append(cache=None, v=None, slot_mapping=None, k_out=torch.zeros(5, 2, 128, dtype=BF))
     assert len(library.calls) == 2
+
+
+def address(library, field):
+    """`field` of the structure that the last call was given."""
+    return next(getattr(a, field) for a in library.calls[-1][1] if hasattr(a, field))
+
+
+def test_replaced_storage_is_used(library):
+    """A cache's or table's tensor replaced, as a whole or in place, is the one
+    that later calls use; one of another form is refused."""
+    cache, rope = dense(), native.Rope(torch.zeros(9, 128))
+    dense_append(cache=cache, rope=rope)
+    assert address(library, "data") == cache.data.data_ptr()
+    assert address(library, "cos_sin") == rope.cos_sin.data_ptr()
+    cache.data, rope.cos_sin = torch.ones((4, 2, 2, 64, 128), dtype=BF), torch.ones(7, 128)
+    dense_append(cache=cache, rope=rope)
+    assert address(library, "data") == cache.data.data_ptr() and address(library, "num_pages") == 4 == cache.num_pages
+    assert address(library, "cos_sin") == rope.cos_sin.data_ptr() and address(library, "num_positions") == 7
+    cache.data.data, rope.cos_sin.data = torch.zeros((4, 2, 2, 64, 128), dtype=BF), torch.zeros(7, 128)
+    dense_append(cache=cache, rope=rope)
+    assert address(library, "data") == cache.data.data_ptr()
+    assert address(library, "cos_sin") == rope.cos_sin.data_ptr()
+    for bad in (cache.data.float(), cache.data[:, :1], cache.data[..., :64], cache.data[:, :, :, ::2], cache.data[0]):
+        with pytest.raises(AssertionError):
+            cache.data = bad
+    for bad in (rope.cos_sin.double(), rope.cos_sin[:, :64], rope.cos_sin[0], rope.cos_sin[:, ::2]):
+        with pytest.raises(AssertionError):
+            rope.cos_sin = bad
+    assert cache.data.shape == (4, 2, 2, 64, 128) and rope.cos_sin.shape == (7, 128)
