@@ -321,7 +321,8 @@ def isoquant_decode_prep(ctx, cache, k, v, slot_mapping, q, q_rot, stream=None):
 
 # The checks of the calls below are tuple comparisons on attributes read once:
 # a decode step's kernels take a few microseconds, which the host has to keep
-# up with.
+# up with.  Every tensor has to lie on the context's device: the kernels would
+# follow any address.
 
 def _address(t):
     return t.data_ptr() if t is not None else None
@@ -337,6 +338,7 @@ def _fits(ctx, cache):
     codes, norms = cache.codes, cache.norms
     assert codes.shape == shape and norms.shape == shape[:3] + shape[4:]
     assert codes.is_contiguous() and norms.is_contiguous()
+    assert codes.get_device() == norms.get_device() == ctx.device
 
 
 def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_rot, stream=None):
@@ -351,6 +353,8 @@ def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, r
     _positions(k_pos, n)
     _positions(q_pos, rows)
     _fits(ctx, cache)
+    assert (k.get_device() == v.get_device() == slot_mapping.get_device() == k_pos.get_device() == q.get_device() ==
+            q_pos.get_device() == q_rot.get_device() == rope.cos_sin.get_device() == ctx.device)
     status = lib().isoquant_decode_prep_rope(ctx.handle, cache.c_struct(), k.data_ptr(), v.data_ptr(), n,
                                              slot_mapping.data_ptr(), k_pos.data_ptr(), q.data_ptr(), _dtype(q), rows,
                                              q.shape[1], q_pos.data_ptr(), rope.c_struct(), q_rot.data_ptr(),
@@ -370,15 +374,19 @@ def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q
     assert k.shape == (n, ctx.num_kv_heads, HEAD_DIM) and k.is_contiguous()
     assert q.shape == q_out.shape == (rows, q.shape[1], HEAD_DIM) and q.is_contiguous() and q_out.is_contiguous()
     assert q.dtype is dtype and q_out.dtype is dtype
+    assert k.get_device() == q.get_device() == q_out.get_device() == ctx.device
     if cache is not None:
         assert v is not None and v.shape == k.shape and v.is_contiguous() and v.dtype is dtype
         assert cache.num_kv_heads == ctx.num_kv_heads
         _positions(slot_mapping, n)
+        assert v.get_device() == slot_mapping.get_device() == cache.data.get_device() == ctx.device
     if rope is not None:
         _positions(k_pos, n)
         _positions(q_pos, rows)
+        assert k_pos.get_device() == q_pos.get_device() == rope.cos_sin.get_device() == ctx.device
     if k_out is not None:
         assert k_out.shape == k.shape and k_out.is_contiguous() and k_out.dtype is dtype
+        assert k_out.get_device() == ctx.device
     status = lib().isoquant_dense_prep(ctx.handle, cache.c_struct() if cache is not None else None, k.data_ptr(),
                                        _address(v), n, _address(slot_mapping), _address(k_pos), q.data_ptr(), _dtype(q),
                                        rows, q.shape[1], _address(q_pos), rope.c_struct() if rope is not None else None,
@@ -404,12 +412,15 @@ def isoquant_dense_attend(ctx, cache, q, page_table, seq_lens, workspace, out, c
     [B][nq][Hq][128] of the cache's dtype; page_table int32 [B][max_pages];
     seq_lens int32 [B]; workspace from alloc_dense_workspace."""
     B, nq, Hq, D = q.shape
-    dtype, max_pages = cache.data.dtype, page_table.shape[1]
+    data = cache.data
+    dtype, max_pages = data.dtype, page_table.shape[1]
     assert D == HEAD_DIM and q.dtype is dtype and q.is_contiguous()
     assert out.shape == q.shape and out.dtype is dtype and out.is_contiguous()
     assert page_table.shape == (B, max_pages) and page_table.dtype is torch.int32 and page_table.is_contiguous()
     assert seq_lens.shape == (B,) and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()
     assert cache.num_kv_heads == ctx.num_kv_heads
+    assert (data.get_device() == q.get_device() == out.get_device() == page_table.get_device() ==
+            seq_lens.get_device() == workspace.get_device() == ctx.device)
     status = lib().isoquant_dense_attend(ctx.handle, cache.c_struct(), q.data_ptr(), B, nq, Hq, page_table.data_ptr(),
                                          max_pages, seq_lens.data_ptr(), 1 if causal else 0, scale,
                                          workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _stream(stream))
@@ -432,6 +443,8 @@ def isoquant_prompt_attend(ctx, q, k, v, cu_seqlens, out, causal=True, scale=0.0
     assert k.dtype is dtype and v.dtype is dtype and out.dtype is dtype
     assert out.shape == q.shape and out.is_contiguous()
     assert cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
+    assert (q.get_device() == k.get_device() == v.get_device() == out.get_device() == cu_seqlens.get_device() ==
+            ctx.device)
     if T <= 1:  # as is that of a single token
         qs, ks, vs = (Hq * HEAD_DIM,), (H * HEAD_DIM,), (H * HEAD_DIM,)
     status = lib().isoquant_prompt_attend(ctx.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), T, Hq,

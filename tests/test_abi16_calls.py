@@ -126,3 +126,57 @@ def test_replaced_storage_is_used(library):
         with pytest.raises(AssertionError):
             rope.cos_sin = bad
     assert cache.data.shape == (4, 2, 2, 64, 128) and rope.cos_sin.shape == (7, 128)
+
+
+class OnGpu(torch.Tensor):
+    """Host memory that says it lies on device 0."""
+
+    def get_device(self):
+        return 0
+
+
+def here(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def test_tensors_of_another_device(library):
+    """Addresses of host memory, or of another device than the context's, reach
+    no kernel: each tensor in turn lies elsewhere."""
+    ctx = Ctx()
+    ctx.device = 0
+    k, q, pos = here(5, 2, 128), here(5, 8, 128), here(5, dtype=torch.int64)
+    rows, ints = here(5, 1, 8, 128), here(5, dtype=torch.int32)
+
+    def cache(codes=here(2, 2, 2, 13, 64, dtype=torch.int32), norms=here(2, 2, 2, 64, dtype=torch.float16)):
+        return native.PagedCache(codes, norms, 64)
+
+    table, data = here(9, 128, dtype=torch.float32), here(2, 2, 2, 64, 128)
+    rope, pages = native.Rope(table), native.DenseCache(data, 64)
+    step = dict(k=k, v=k, slot_mapping=pos, k_pos=pos, q=q, q_pos=pos, rope=rope)
+    calls = (
+        (native.isoquant_decode_prep_rope, dict(step, cache=cache(), q_rot=here(5, 8, 128, dtype=torch.float32))),
+        (native.isoquant_dense_prep, dict(step, cache=pages, q_out=q, k_out=k)),
+        (native.isoquant_dense_attend, dict(cache=pages, q=rows, page_table=here(5, 3, dtype=torch.int32),
+                                            seq_lens=ints, workspace=ints, out=rows)),
+        (native.isoquant_prompt_attend, dict(q=q, k=k, v=k, cu_seqlens=ints, out=q)),
+    )
+    elsewhere = {id(rope): [native.Rope(table.as_subclass(torch.Tensor))],
+                 id(pages): [native.DenseCache(data.as_subclass(torch.Tensor), 64)]}
+    for call, args in calls:
+        call(ctx, stream=0, **args)
+        count = len(library.calls)
+        for name, value in args.items():
+            others = elsewhere.get(id(value))
+            if isinstance(value, torch.Tensor):
+                others = [value.as_subclass(torch.Tensor)]
+            elif others is None:
+                others = [cache(codes=value.codes.as_subclass(torch.Tensor)),
+                          cache(norms=value.norms.as_subclass(torch.Tensor))]
+            for other in others:
+                with pytest.raises(AssertionError):
+                    call(ctx, stream=0, **dict(args, **{name: other}))
+        assert len(library.calls) == count
+        second = Ctx()
+        second.device = 1
+        with pytest.raises(AssertionError):
+            call(second, stream=0, **args)
