@@ -130,9 +130,16 @@ def _check(status, what):
         raise IsoquantError(status, what)
 
 
+# a device's current stream without building a Stream object; not public, so
+# calls do without it where torch has none
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:  # the current device's current stream (without building a Stream object)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if stream is None:  # the current device's current stream
+        if _raw_stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))

@@ -180,3 +180,17 @@ def test_tensors_of_another_device(library):
         second.device = 1
         with pytest.raises(AssertionError):
             call(second, stream=0, **args)
+
+
+def test_current_stream(monkeypatch):
+    """The current device's current stream, with torch's short way to it and without."""
+    class Stream:
+        cuda_stream = 4321
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(native, "_raw_stream", lambda device: 1000 + device)
+    assert native._stream(None).value == 1003
+    monkeypatch.setattr(native, "_raw_stream", None)
+    assert native._stream(None).value == 4321
+    assert native._stream(77).value == 77
