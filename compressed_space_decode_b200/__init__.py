@@ -184,10 +184,36 @@ class PagedCache:
 
     def __init__(self, codes, norms, page_size):
         assert codes.dtype == torch.int32 and norms.dtype == torch.float16
+        self._norms = norms
         self.codes = codes
-        self.norms = norms
         self.num_pages = codes.shape[0]
         self.page_size = page_size
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, codes):
+        self._codes = codes
+        self._note_form()
+
+    @property
+    def norms(self):
+        return self._norms
+
+    @norms.setter
+    def norms(self, norms):
+        self._norms = norms
+        self._note_form()
+
+    def _note_form(self):
+        """The codes' shape and the device, once for the calls that compare
+        them with the context's; None for tensors that do not belong together."""
+        codes, norms = self._codes, self._norms
+        whole = (codes.is_contiguous() and norms.is_contiguous() and norms.shape == codes.shape[:3] + codes.shape[4:] and
+                 codes.get_device() == norms.get_device())
+        self._form = (*codes.shape, codes.get_device()) if whole else None
 
     @staticmethod
     def allocate(num_kv_heads, num_pages, page_size, device="cuda", bits=3):
@@ -341,11 +367,7 @@ def _positions(t, n):
 
 def _fits(ctx, cache):
     """The kernels address a packed cache by the context's heads and code width."""
-    shape = (cache.num_pages, 2, ctx.num_kv_heads, WORDS_FOR[ctx.bits], cache.page_size)
-    codes, norms = cache.codes, cache.norms
-    assert codes.shape == shape and norms.shape == shape[:3] + shape[4:]
-    assert codes.is_contiguous() and norms.is_contiguous()
-    assert codes.get_device() == norms.get_device() == ctx.device
+    assert cache._form == (cache.num_pages, 2, ctx.num_kv_heads, WORDS_FOR[ctx.bits], cache.page_size, ctx.device)
 
 
 def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q_rot, stream=None):
