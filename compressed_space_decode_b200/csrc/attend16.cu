@@ -36,11 +36,16 @@
 //     row sees whole: rows behind the last visible token are cleared
 //     (neighbouring sequences, padding, stale pages: 0 x NaN would be NaN) and
 //     non-finite elements taken out; the rows that do see such an element get
-//     it added at the end.
-// Prompts of 32768 tokens, 32 and 8 heads: 1060 (power-capped) to 1250 TFLOP/s.  What bounds
+//     it added at the end.  Of tokens that every row sees they stay in: a sum
+//     that comes out NaN is looked up in the values then.
+// Prompts of 32768 tokens, 32 and 8 heads: 1040 (power-capped) to 1240 TFLOP/s.  What bounds
 // it: the products' issue.  In isolation the 16 products of a side and tile
 // take 1027 cycles; here 1690, their warps sharing issue slots and tensor
 // memory with the softmax (removing the exponentials gains 3 %, the copies 2 %).
+// Weights keep 8 bits (bf16) or 11 (fp16) in the prompts' product with V: a
+// second operand for the remainders would be half as many products again.
+// Over the cache, which is bound by its bytes, bf16 weights keep 16; fp16's 11
+// are off by no more than the result's own rounding.
 // All waits are bounded; after one expires every role leaves its loop.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -768,8 +773,8 @@ struct Loader {
   }
 };
 
-// Tokens of a copied box, which a page of any size holds whole (8 read slower:
-// 285 us for 16 x 32768 tokens; 16: 197; 32 and 128: 186).
+// Tokens of a copied box, which a page of any size holds whole (16 x 32768
+// tokens: 8 tokens a box 287 us, 16 188, 32 162, 128 161).
 constexpr int kBox = 32;
 // The loader warp over the cache: the segments' queries into q_bufs buffers
 // whose 64-dim halves are p.q_half bytes, key and value tiles into the ring.
@@ -1367,8 +1372,9 @@ struct Cols {
   static constexpr int kThreads = (4 + NR / kSide * 4) * 32;
   static constexpr int kN = kLo ? 2 * NR : NR;         // columns of O^T
   static constexpr int kQBufs = NR == 64 ? 1 : 2;
-  static constexpr int kPBufs = NR == 64 ? 1 : 2;
-  // 16 x 32768 tokens: 4 slots 186 us, 5 186, 6 200; 4 long contexts: 246, 260, 272
+  static constexpr int kPBufs = NR == 64 ? 1 : 2;  // (two for 64 rows fit, and gain nothing: 113 -> 114 us)
+  // 16 x 32768 tokens: 4 and 5 slots 162 us; 4 long contexts: 222 and 221;
+  // 16-token chunks: 113 and 109 (6 slots were slower: 200 when 4 were 186)
   static constexpr int kSlots = 4;
   static constexpr int kQBytes = NR * kD * 2;
   static constexpr int kPBytes = kN * kTile * 2;
@@ -1900,8 +1906,9 @@ cudaError_t launch_prompt_attend(const isoquant_ctx *ctx, const void *q, const v
   auto jobs = [&](int sides) { return (static_cast<int64_t>(n_tok) / (sides * p.tok) + batch) * p.H; };
   // Where two-sided jobs would leave SMs idle, jobs of one row tile whose key
   // tiles the sides share are half as long (7237 tokens, 2 and 1 heads, 57
-  // jobs: 147 -> 96 us; 114 jobs 47.9 -> 44.8, 126 jobs 82 -> 80), but read each
-  // key tile twice as often (136 short jobs 23.3 -> 25.6, 376 jobs 105 -> 123).
+  // jobs: 143 -> 81 us; 16384, 1 head, 65 jobs: 263 -> 169; 114 jobs of three
+  // prompts: 41 -> 35), but read each key tile twice as often (136 short jobs
+  // 17.9 -> 20.9, 252 jobs 56 -> 60, 316 jobs 73 -> 84).
   p.sides = jobs(2) < ctx->num_sms * 3 / 4 ? 1 : 2;
   const int64_t grid = jobs(p.sides);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;

@@ -817,7 +817,8 @@ __global__ void __launch_bounds__(256) k_decode_prep(const CompressArgs c, const
 // vectors at a time through the two layouts of the compress path: strips of
 // g.strip of a KV head's (row, group head) vectors, so that the head's SO(4)
 // blocks are loaded once.  8192 rows of 32 heads: 412 us with one warp per
-// vector as in k_decode_prep, 65 us so (201 MB; instruction issue bounds it).
+// vector as in k_decode_prep, 53 us so (201 MB).  Latency bounds it: 14 warps an
+// SM on long dependent chains, an instruction issued in 0.43 of the cycles.
 // The result's 64 bytes per lane go out as two 32-byte stores (whole sectors).
 __device__ __forceinline__ void store8(float *dst, const float *v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),

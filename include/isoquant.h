@@ -175,7 +175,8 @@ int isoquant_cache_bytes(const isoquant_ctx *ctx, int num_pages, int page_size,
  *          contiguous, 8-byte aligned.
  *   slot_mapping: device int64 [n_tok], slot = page * page_size + offset;
  *          a negative slot skips that token; a slot beyond the cache sets
- *          ISOQUANT_DEVERR_SLOT_RANGE and is skipped.
+ *          ISOQUANT_DEVERR_SLOT_RANGE and is skipped.  Of two tokens of a
+ *          call with one slot either may stay, word by word.
  * Writes 13 code words and one fp16 norm per (token, head, K/V).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
 int isoquant_compress_kv(isoquant_ctx *ctx, const isoquant_cache *cache,
@@ -282,7 +283,8 @@ int isoquant_decode_prep_rope(isoquant_ctx *ctx, const isoquant_cache *cache,
 /* The same preparation for a 16-bit cache, in one launch: append
  * rope(k, k_pos) and v at their slots and write q_out = rope(q, q_pos), each
  * computed in fp32 and rounded once to `dtype` (BF16 or F16, the cache's).
- *   k, v, slot_mapping, q: as isoquant_decode_prep, 16-byte aligned
+ *   k, v, slot_mapping, q: as isoquant_decode_prep, 16-byte aligned (of
+ *          two tokens with one slot either may stay, 16 bytes by 16)
  *   rope:  NULL appends and copies without a rotation; k_pos and q_pos are
  *          then not looked at and may be NULL
  *   k_out: device [n_tok][num_kv_heads][128] of `dtype` or NULL: every
@@ -312,7 +314,9 @@ int isoquant_dense_workspace_size(const isoquant_ctx *ctx, int batch, int nq,
 /* Attention of each sequence's newest tokens over a 16-bit paged cache,
  * split over the context and joined: o = sum_t p_t v_t, p = softmax of
  * scale <q, k_t> over the visible tokens; scores, softmax statistics and
- * sums in fp32, the result rounded once.
+ * sums in fp32, the result rounded once.  For the product with v a softmax
+ * weight is held as two bf16 parts (BF16 pages: 16 bits) or rounded to fp16
+ * (F16 pages: 11 bits, below 2^-21 of the row's reference fewer).
  *   q:   device [batch][nq][num_q_heads][128] of the cache's dtype,
  *        16-byte aligned (rotated by position already, if at all)
  *   out: device, same shape and dtype, 16-byte aligned
@@ -353,7 +357,7 @@ int isoquant_dense_attend(isoquant_ctx *ctx, const isoquant_dense_cache *cache,
  *      aligned, apart from the inputs; rows of no sequence are left as they
  *      were (a row whose every score is -inf outputs zeros)
  * Scores, softmax statistics and sums in fp32; softmax weights are rounded
- * to `dtype` for the product with v.  NaN and infinite values reach the rows
+ * to `dtype` for the product with v (8 or 11 bits).  NaN and infinite values reach the rows
  * that see their token, no others, as in isoquant_dense_attend.  One kernel launch, no workspace.
  * num_q_heads / num_kv_heads at most 128.  Errors: INVALID_ARG, UNSUPPORTED
  * (dtype, group size), ALIGNMENT, CUDA. */
