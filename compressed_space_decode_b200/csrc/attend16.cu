@@ -1188,37 +1188,36 @@ __global__ void __launch_bounds__(kThreads16, 1)
     const int r_tok = r / p.GB, r_head = r - r_tok * p.GB;
     uint32_t n_s = 0, n_o1 = 0, n_o = 0;
     bool ok = true;
-    // one row's sum of products, times f, plus what the guards took out; a NaN
-    // of the sum stays in `worst`
-    auto finish = [&](uint32_t k, int lim, float (&o)[32], int col, float f, float &worst) {
+    // one row's sum of products, times f; a NaN of the sum stays in `worst`
+    auto finish = [&](float (&o)[32], float f, float &worst) {
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         o[i] *= f;
         o[i + 1] *= f;
         worst = max3_nan(worst, o[i], o[i + 1]);
       }
-      if (*nonfinite == static_cast<int>(k) + 1) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = with_nonfinite(o[i], bad, col + i, lim);
-      }
     };
     auto passed = [&](uint32_t k) {  // segment k's marks have been read
       __syncwarp();
       if (lane == 0) *const_cast<volatile int *>(&flags->done[warp - 4]) = static_cast<int>(k) + 1;
     };
-    // Infinities that the products lost, put right where the row was stored
-    // (rare: a loop that takes no room in the code above).  sees: a valid row
-    // whose sum of weights is a number; lim: 0 for a row that is zero.
-    auto repair = [&](const Segment &s, uint32_t k, bool sees, int lim, auto *dst) {
+    // Non-finite values, added where the row was stored: those that the guard
+    // took out, and infinities that the products lost (rare: a loop that takes
+    // no room in the code above).  sum: of the row's weights; a row without
+    // weight is zero and stays so.
+    auto repair = [&](const Segment &s, uint32_t k, bool valid, int lim, float sum, float worst, bool whole, auto *dst) {
+      const bool marked = *nonfinite == static_cast<int>(k) + 1, lost = valid && sum == sum && isnan(worst);
+      const bool any_lost = __any_sync(0xffffffffu, lost);
+      if (!marked && !any_lost) return;
       const int t0 = s.j0 * kTile, end = min(all_see(p, s), t0 + tiles(s) * kTile);
-      const uint32_t seen = values_seen<T, kPaged>(p, s, t0, end);
+      const uint32_t seen = any_lost ? values_seen<T, kPaged>(p, s, t0, end) : 0;
       for (int d = 0; d < kD; ++d) {
         const uint32_t kinds = kinds_of(seen, d);
-        if (sees && kinds != 0 && isnan(static_cast<float>(dst[d]))) {
-          float y = lim > 0 ? nonfinite_sum(kinds) : 0.f;
-          if (*nonfinite == static_cast<int>(k) + 1) y = with_nonfinite(y, bad, d, lim);
-          dst[d] = y;
-        }
+        if (!valid) continue;
+        float y = static_cast<float>(dst[d]);
+        if (lost && kinds != 0 && isnan(y)) y = nonfinite_sum(kinds);
+        if (marked) y = with_nonfinite(y, bad, d, lim);
+        dst[d] = whole && sum == 0.f ? 0.f : y;
       }
     };
     auto store16 = [&](T *dst, const float (&o)[32]) {
@@ -1264,17 +1263,15 @@ __global__ void __launch_bounds__(kThreads16, 1)
         const float inv = l != 0.f ? 1.f / l : 0.f;
         T *dst = static_cast<T *>(p.out) +
                  (static_cast<int64_t>(s.kv0 + qi) * p.Hq + static_cast<int64_t>(s.h) * p.G + hq) * kD;
-        const int lim0 = l != 0.f ? lim : 0;  // every score -inf: zero
         float worst = 0.f;
 #pragma unroll
         for (int col = 0; col < kD; col += 32) {
           float o[32];
           tmem_ld32(to + col, o);
-          finish(k, lim0, o, col, inv, worst);
+          finish(o, inv, worst);
           if (valid) store16(dst + col, o);
         }
-        const bool sees = valid && l == l;
-        if (__any_sync(0xffffffffu, sees && isnan(worst))) repair(s, k, sees, lim0, dst);
+        repair(s, k, valid, lim, l, worst, true, dst);
         tc_fence_before();
         passed(k);
       } else if (x == 1) {
@@ -1308,7 +1305,6 @@ __global__ void __launch_bounds__(kThreads16, 1)
         T *dst = static_cast<T *>(p.out) + (row * p.Hq +
                                             static_cast<int64_t>(s.h) * p.G + hq) * kD;
         if (valid && !whole) *reinterpret_cast<float2 *>(rec + 2 * r) = make_float2(m, l);
-        const int lim0 = !whole || l != 0.f ? lim : 0;
         float worst = 0.f;
 #pragma unroll
         for (int col = 0; col < kD; col += 32) {
@@ -1320,7 +1316,7 @@ __global__ void __launch_bounds__(kThreads16, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
           }
-          finish(k, lim0, o, col, whole ? inv : 1.f, worst);
+          finish(o, whole ? inv : 1.f, worst);
           if (valid) {
             if (whole) {
               store16(dst + col, o);
@@ -1332,11 +1328,8 @@ __global__ void __launch_bounds__(kThreads16, 1)
             }
           }
         }
-        const bool sees = valid && l == l;
-        if (__any_sync(0xffffffffu, sees && isnan(worst))) {
-          if (whole) repair(s, k, sees, lim0, dst);
-          else repair(s, k, sees, lim0, rec + 2 * p.row_stride + r * kD);
-        }
+        if (whole) repair(s, k, valid, lim, l, worst, true, dst);
+        else repair(s, k, valid, lim, l, worst, false, rec + 2 * p.row_stride + r * kD);
         tc_fence_before();
         passed(k);
         if (lane == 0) mbar_arrive(&bars.seg_done);
