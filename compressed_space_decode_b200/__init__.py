@@ -245,6 +245,7 @@ class DenseCache:
         self._data = data
         self.num_kv_heads = data.shape[2]
         self.num_pages = data.shape[0]
+        self._device = data.get_device()
         self._c = _DenseCache(data.data_ptr(), _dtype(data), self.num_pages, self.page_size)
 
     @staticmethod
@@ -276,6 +277,7 @@ class Rope:
         assert cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
         assert cos_sin.dim() == 2 and cos_sin.shape[1] == self.rot_dim
         self._cos_sin = cos_sin
+        self._device = cos_sin.get_device()
         self._c = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], self.rot_dim, int(self.interleaved))
 
     @staticmethod
@@ -383,7 +385,7 @@ def isoquant_decode_prep_rope(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, r
     _positions(q_pos, rows)
     _fits(ctx, cache)
     assert (k.get_device() == v.get_device() == slot_mapping.get_device() == k_pos.get_device() == q.get_device() ==
-            q_pos.get_device() == q_rot.get_device() == rope.cos_sin.get_device() == ctx.device)
+            q_pos.get_device() == q_rot.get_device() == rope._device == ctx.device)
     status = lib().isoquant_decode_prep_rope(ctx.handle, cache.c_struct(), k.data_ptr(), v.data_ptr(), n,
                                              slot_mapping.data_ptr(), k_pos.data_ptr(), q.data_ptr(), _dtype(q), rows,
                                              q.shape[1], q_pos.data_ptr(), rope.c_struct(), q_rot.data_ptr(),
@@ -408,11 +410,11 @@ def isoquant_dense_prep(ctx, cache, k, v, slot_mapping, k_pos, q, q_pos, rope, q
         assert v is not None and v.shape == k.shape and v.is_contiguous() and v.dtype is dtype
         assert cache.num_kv_heads == ctx.num_kv_heads
         _positions(slot_mapping, n)
-        assert v.get_device() == slot_mapping.get_device() == cache.data.get_device() == ctx.device
+        assert v.get_device() == slot_mapping.get_device() == cache._device == ctx.device
     if rope is not None:
         _positions(k_pos, n)
         _positions(q_pos, rows)
-        assert k_pos.get_device() == q_pos.get_device() == rope.cos_sin.get_device() == ctx.device
+        assert k_pos.get_device() == q_pos.get_device() == rope._device == ctx.device
     if k_out is not None:
         assert k_out.shape == k.shape and k_out.is_contiguous() and k_out.dtype is dtype
         assert k_out.get_device() == ctx.device
@@ -441,14 +443,13 @@ def isoquant_dense_attend(ctx, cache, q, page_table, seq_lens, workspace, out, c
     [B][nq][Hq][128] of the cache's dtype; page_table int32 [B][max_pages];
     seq_lens int32 [B]; workspace from alloc_dense_workspace."""
     B, nq, Hq, D = q.shape
-    data = cache.data
-    dtype, max_pages = data.dtype, page_table.shape[1]
+    dtype, max_pages = cache.data.dtype, page_table.shape[1]
     assert D == HEAD_DIM and q.dtype is dtype and q.is_contiguous()
     assert out.shape == q.shape and out.dtype is dtype and out.is_contiguous()
     assert page_table.shape == (B, max_pages) and page_table.dtype is torch.int32 and page_table.is_contiguous()
     assert seq_lens.shape == (B,) and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()
     assert cache.num_kv_heads == ctx.num_kv_heads
-    assert (data.get_device() == q.get_device() == out.get_device() == page_table.get_device() ==
+    assert (cache._device == q.get_device() == out.get_device() == page_table.get_device() ==
             seq_lens.get_device() == workspace.get_device() == ctx.device)
     status = lib().isoquant_dense_attend(ctx.handle, cache.c_struct(), q.data_ptr(), B, nq, Hq, page_table.data_ptr(),
                                          max_pages, seq_lens.data_ptr(), 1 if causal else 0, scale,
